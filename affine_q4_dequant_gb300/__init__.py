@@ -12,6 +12,9 @@ PyTorch supplies device memory and streams. Storage conventions:
   s, b      torch.bfloat16 (or int16/uint16 bit views) [rows][in_dim/64]
   x         torch.float16 (or int16/uint16 bit views) [nb][in_dim]
   y         torch.float32 [nb][out_dim]
+The 8-bit form (the *_fp8 functions):
+  q, w8     torch.float8_e4m3fn (or uint8 views) activations [nb][dim], weights [out_dim][in_dim]
+  scale     torch.float32 [nb][ceil(dim/128)], w_scale [ceil(out_dim/128)][ceil(in_dim/128)]
 """
 
 from __future__ import annotations
@@ -29,7 +32,9 @@ __all__ = [
     "gemv_experts_gate_up_silu",
     "gemv_rmsnorm",
     "gemv_rmsnorm_grouped", "gemv_inject_rmsnorm_grouped", "gemv_gate_up_silu", "gemv_rmsnorm_gate_up_silu", "decode_mlp", "lowbit_pack",
-    "gemv_lowbit", "quantize", "gemv_f32x", "silu_mul_xsum", "moe_combine", "check_device_error", "debug_withhold_stage",
+    "gemv_lowbit", "quantize", "gemv_f32x", "silu_mul_xsum", "moe_combine",
+    "quantize_fp8", "add_rmsnorm_fp8", "dequant_fp8", "gemm_fp8", "gemm_fp8_gate_up_silu", "mlp_fp8",
+    "check_device_error", "debug_withhold_stage",
     "gemv_kernel_choice",
     "STATUS", "MAX_SEGMENTS",
 ]
@@ -79,6 +84,12 @@ def _load() -> ctypes.CDLL:
         "q4a_gemv_inject_rmsnorm_grouped": (I32, [P, P, P, P, P, P, P, P, P, F, F, I32, I32, I64, I64, P]),
         "q4a_silu_mul_xsum": (I32, [P, P, P, I64, I64, P]),
         "q4a_moe_combine": (I32, [P, P, P, P, I32, I32, I64, I64, P, P, P, P]),
+        "q4a_quantize_fp8": (I32, [P, P, P, I32, I64, I64, P]),
+        "q4a_add_rmsnorm_fp8": (I32, [P, P, P, P, I32, P, I32, P, F, F, I64, I64, P]),
+        "q4a_dequant_fp8": (I32, [P, P, P, P, P, I64, I64, P]),
+        "q4a_gemm_fp8": (I32, [P, I32, P, P, P, P, I64, I64, I64, P]),
+        "q4a_gemm_fp8_gate_up_silu": (I32, [P, P, P, P, P, P, I64, I64, I64, P]),
+        "q4a_mlp_fp8": (I32, [P, I32, P, P, P, P, P, P, I32, P, I32, P, F, F, P, P, P, P, I64, I64, I64, P]),
         "q4a_check_device_error": (I32, [P]),
         "q4a_debug_withhold_stage": (I32, [I32]),
         "q4a_gemv_kernel_choice": (I32, [P, P, I32, I64, I64]),
@@ -119,6 +130,8 @@ _F16 = (torch.float16, torch.int16, torch.uint16)
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
+_F8 = (torch.float8_e4m3fn, torch.uint8)
+_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}   # q4a_type
 _ANY = None   # any dtype (prefetch hints)
 _NULL = ctypes.c_void_p(0)
 
@@ -465,6 +478,142 @@ def moe_combine(y: torch.Tensor, slot: torch.Tensor, w: torch.Tensor, y_shared: 
     _check("q4a_moe_combine", _lib.q4a_moe_combine(po, py, ps, pw, int(n_tok), int(top_k), int(n_slots), int(hidden),
                                                    pys, pg, px, _stream(stream)))
     return out
+
+
+def _type(t, name: str) -> int:
+    """The q4a_type of a tensor (or dtype) that an 8-bit entry point takes in more than one type."""
+    dtype = t.dtype if isinstance(t, torch.Tensor) else t
+    if dtype not in _TYPES:
+        raise TypeError(f"{name}: dtype {dtype} not in {tuple(_TYPES)}")
+    return _TYPES[dtype]
+
+
+def _empty_on(stream, shape, dtype, like):
+    """A buffer from the memory pool of the stream that will use it: a buffer of another stream's
+    pool could be handed on there while this stream's kernels still run."""
+    if stream is None:
+        return _empty(shape, dtype, like)
+    with torch.cuda.stream(stream):
+        return _empty(shape, dtype, like)
+
+
+def _fp8_rows(stream, q, scale, nb: int, dim: int, like, qname: str = "q", sname: str = "scale"):
+    """The codes [nb][dim] and scales [nb][ceil(dim/128)] of 8-bit rows, allocated where not given,
+    and their specs."""
+    q = _empty_on(stream, (nb, dim), torch.float8_e4m3fn, like) if q is None else q
+    blocks = (dim + 127) // 128
+    scale = _empty_on(stream, (nb, blocks), torch.float32, like) if scale is None else scale
+    return q, scale, ((q, qname, _F8, (nb, dim)), (scale, sname, _F32, (nb, blocks)))
+
+
+def _fp8_mat(w, w_scale, out_dim: int, in_dim: int, wname: str = "w", sname: str = "w_scale"):
+    """Specs of an 8-bit matrix: codes [out_dim][in_dim], scales per block of 128 x 128."""
+    return ((w, wname, _F8, (out_dim, in_dim)),
+            (w_scale, sname, _F32, ((out_dim + 127) // 128, (in_dim + 127) // 128)))
+
+
+def quantize_fp8(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Tensor | None = None, stream=None):
+    """Activations x [nb][dim] (fp32, fp16 or bf16) as e4m3 codes with a scale per 128 columns:
+    (q float8_e4m3fn [nb][dim], scale fp32 [nb][ceil(dim/128)])."""
+    nb, dim = _dims(x, "x")
+    xt = _type(x, "x")
+    q, scale, specs = _fp8_rows(stream, q, scale, nb, dim, x)
+    pq, ps, px = _ptrs(*specs, (x, "x", None, None))
+    _check("q4a_quantize_fp8", _lib.q4a_quantize_fp8(pq, ps, px, xt, nb, dim, _stream(stream)))
+    return q, scale
+
+
+def add_rmsnorm_fp8(x, norm_w, residual: torch.Tensor | None = None, eps: float = 1e-6, shift: float = 0.0,
+                    q: torch.Tensor | None = None, scale: torch.Tensor | None = None,
+                    x_new: torch.Tensor | None = None, want_x_new: bool = True, stream=None):
+    """The RMSNorm of x' = x + residual in 8 bits: (q, scale, x_new). x_new is x' in the residual's
+    type, and may be the residual itself (in place); it is None without a residual or when
+    want_x_new is False."""
+    nb, dim = _dims(x, "x")
+    xt = _type(x, "x")
+    q, scale, specs = _fp8_rows(stream, q, scale, nb, dim, x)
+    rt = 0
+    if residual is not None:
+        rt = _type(residual, "residual")
+        if x_new is None and want_x_new:
+            x_new = _empty_on(stream, (nb, dim), residual.dtype, x)
+    elif x_new is not None:
+        raise ValueError("x_new needs a residual")
+    pq, ps, pn, px, pr, pw = _ptrs(
+        *specs, None if x_new is None else (x_new, "x_new", (residual.dtype,), (nb, dim)), (x, "x", None, None),
+        None if residual is None else (residual, "residual", None, (nb, dim)), (norm_w, "norm_w", _BF16, (dim,)))
+    _check("q4a_add_rmsnorm_fp8", _lib.q4a_add_rmsnorm_fp8(pq, ps, pn, px, xt, pr, rt, pw, float(eps), float(shift),
+                                                           nb, dim, _stream(stream)))
+    return q, scale, x_new
+
+
+def dequant_fp8(w, s, b, out: torch.Tensor | None = None, scale: torch.Tensor | None = None, stream=None):
+    """Packed 4-bit weights (as gemv()) laid out in e4m3: (w8 float8_e4m3fn [rows][in], w_scale fp32
+    [ceil(rows/128)][ceil(in/128)])."""
+    rows, half = _dims(w, "w")
+    in_dim = 2 * half
+    out = _empty_on(stream, (rows, in_dim), torch.float8_e4m3fn, w) if out is None else out
+    scale = _empty_on(stream, ((rows + 127) // 128, (in_dim + 127) // 128), torch.float32, w) if scale is None else scale
+    po, pc, pw, ps, pb = _ptrs(*_fp8_mat(out, scale, rows, in_dim, "out", "scale"), *_mat(w, s, b, rows, in_dim))
+    _check("q4a_dequant_fp8", _lib.q4a_dequant_fp8(po, pc, pw, ps, pb, rows, in_dim, _stream(stream)))
+    return out, scale
+
+
+def gemm_fp8(w, w_scale, x, x_scale, out: torch.Tensor | None = None, out_dtype=torch.float32, stream=None):
+    """y = W x [nb][out_dim] from e4m3 weights and activations with their block scales; out_dtype is
+    float32, float16 or bfloat16 (the type of out, where given)."""
+    out_dim = _dims(w, "w")[0]
+    nb, in_dim = _dims(x, "x")
+    yt = _type(out_dtype if out is None else out, "y")
+    out = _empty_on(stream, (nb, out_dim), out_dtype, x) if out is None else out
+    _, _, xs = _fp8_rows(stream, x, x_scale, nb, in_dim, x, "x", "x_scale")
+    py, pw, pws, px, pxs = _ptrs((out, "y", None, (nb, out_dim)), *_fp8_mat(w, w_scale, out_dim, in_dim), *xs)
+    _check("q4a_gemm_fp8", _lib.q4a_gemm_fp8(py, yt, pw, pws, px, pxs, nb, out_dim, in_dim, _stream(stream)))
+    return out
+
+
+def gemm_fp8_gate_up_silu(w, w_scale, x, x_scale, q: torch.Tensor | None = None, scale: torch.Tensor | None = None,
+                          stream=None):
+    """h = silu(W_gate x) * (W_up x) in 8 bits: (q [nb][inter], scale [nb][inter/128]). w holds the
+    inter gate rows, then the up rows; inter is a multiple of 128."""
+    nb, in_dim = _dims(x, "x")
+    inter = _dims(w, "w")[0] // 2
+    q, scale, qs = _fp8_rows(stream, q, scale, nb, inter, x)
+    _, _, xs = _fp8_rows(stream, x, x_scale, nb, in_dim, x, "x", "x_scale")
+    pq, ps, pw, pws, px, pxs = _ptrs(*qs, *_fp8_mat(w, w_scale, 2 * inter, in_dim), *xs)
+    _check("q4a_gemm_fp8_gate_up_silu", _lib.q4a_gemm_fp8_gate_up_silu(pq, ps, pw, pws, px, pxs, nb, inter, in_dim,
+                                                                       _stream(stream)))
+    return q, scale
+
+
+def mlp_fp8(x, norm_w, w_gu, ws_gu, w_dn, ws_dn, residual: torch.Tensor | None = None, eps: float = 1e-6,
+            shift: float = 0.0, out: torch.Tensor | None = None, out_dtype=torch.float32,
+            x_new: torch.Tensor | None = None, want_x_new: bool = True, n=None, h=None, stream=None):
+    """A layer's gated MLP on 8-bit operands: add_rmsnorm_fp8, gemm_fp8_gate_up_silu, gemm_fp8.
+    Returns (y [nb][hidden], x_new). n and h, the normalised rows and the inner activations, may be
+    given as pairs (codes, scales) to write them into."""
+    nb, hidden = _dims(x, "x")
+    inter = _dims(w_gu, "w_gu")[0] // 2
+    xt = _type(x, "x")
+    yt = _type(out_dtype if out is None else out, "y")
+    out = _empty_on(stream, (nb, hidden), out_dtype, x) if out is None else out
+    _, _, ns = _fp8_rows(stream, *(n or (None, None)), nb, hidden, x, "n", "n_scale")
+    _, _, hs = _fp8_rows(stream, *(h or (None, None)), nb, inter, x, "h", "h_scale")
+    rt = 0
+    if residual is not None:
+        rt = _type(residual, "residual")
+        if x_new is None and want_x_new:
+            x_new = _empty_on(stream, (nb, hidden), residual.dtype, x)
+    elif x_new is not None:
+        raise ValueError("x_new needs a residual")
+    py, pxn, pn, pns, ph, phs, px, pr, pw, pgu, psg, pdn, psd = _ptrs(
+        (out, "y", None, (nb, hidden)), None if x_new is None else (x_new, "x_new", (residual.dtype,), (nb, hidden)),
+        *ns, *hs, (x, "x", None, None), None if residual is None else (residual, "residual", None, (nb, hidden)),
+        (norm_w, "norm_w", _BF16, (hidden,)), *_fp8_mat(w_gu, ws_gu, 2 * inter, hidden, "w_gu", "ws_gu"),
+        *_fp8_mat(w_dn, ws_dn, hidden, inter, "w_dn", "ws_dn"))
+    _check("q4a_mlp_fp8", _lib.q4a_mlp_fp8(py, yt, pxn, pn, pns, ph, phs, px, xt, pr, rt, pw, float(eps), float(shift),
+                                           pgu, psg, pdn, psd, nb, hidden, inter, _stream(stream)))
+    return out, x_new
 
 
 def check_device_error(stream=None) -> None:

@@ -4,6 +4,7 @@
 
 #include <vector>
 
+#include "q4a_fp8.h"
 #include "q4a_internal.h"
 #include "q4a_prefill.h"
 
@@ -563,6 +564,150 @@ q4a_status q4a_moe_combine(float* out, const float* y, const int32_t* slot, cons
         return Q4A_ERR_ALIGN;
     return launch_moe_combine(out, y, slot, w, n_tok, top_k, n_slots, hidden, y_shared, y_shared ? gate : nullptr,
                               y_shared ? x : nullptr, (cudaStream_t)stream);
+}
+
+}  // extern "C"
+
+// ---- the 8-bit form ----------------------------------------------------------------------
+
+namespace q4a {
+namespace {
+
+bool type_ok(q4a_type t) { return t == Q4A_F32 || t == Q4A_F16 || t == Q4A_BF16; }
+
+// Whether [a, a + an) and [b, b + bn) share a byte.
+bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
+}
+
+// Rows of 8-bit activations: sizes and the two output (or input) buffers.
+q4a_status check_fp8_rows(const uint8_t* q, const float* scale, int64_t nb, int64_t dim) {
+    if (!q || !scale) return Q4A_ERR_NULL;
+    if (nb < 1 || dim < 16 || dim % 16 != 0) return Q4A_ERR_SHAPE;
+    if (nb > ((int64_t)1 << 31) - 1 || dim > kFp8MaxDim) return Q4A_ERR_UNSUPPORTED;
+    if (!aligned(q, 16) || !aligned(scale, 4)) return Q4A_ERR_ALIGN;
+    return Q4A_OK;
+}
+
+q4a_status check_add_rmsnorm(const Fp8Norm& n) {
+    if (!n.x || !n.norm_w) return Q4A_ERR_NULL;
+    q4a_status st = check_fp8_rows(n.q, n.scale, n.nb, n.dim);
+    if (st != Q4A_OK) return st;
+    if (!type_ok(n.x_type) || (n.residual && !type_ok(n.res_type)) || !(n.eps >= 0.0f)) return Q4A_ERR_SHAPE;
+    if (n.x_new && !n.residual) return Q4A_ERR_SHAPE;
+    if (!aligned(n.x, 16) || !aligned(n.norm_w, 16) || (n.residual && !aligned(n.residual, 16)) ||
+        (n.x_new && !aligned(n.x_new, 16)))
+        return Q4A_ERR_ALIGN;
+    // a row's threads read their elements of x and of the residual before they write x_new there:
+    // the very same buffer is safe, a shifted one is not
+    const int64_t xb = n.nb * n.dim * fp8_type_bytes(n.x_type);
+    const int64_t rb = n.residual ? n.nb * n.dim * fp8_type_bytes(n.res_type) : 0;
+    if (n.x_new) {
+        if (n.x_new != n.residual && overlap(n.x_new, rb, n.residual, rb)) return Q4A_ERR_SHAPE;
+        if (!(n.x_new == n.x && n.x_type == n.res_type) && overlap(n.x_new, rb, n.x, xb)) return Q4A_ERR_SHAPE;
+    }
+    return Q4A_OK;
+}
+
+// A block-scaled product: sizes and operands (the caller checks its outputs).
+q4a_status check_fp8_product(const uint8_t* w, const float* w_scale, const uint8_t* x, const float* x_scale,
+                             int64_t nb, int64_t out_dim, int64_t in_dim) {
+    if (!w || !w_scale || !x || !x_scale) return Q4A_ERR_NULL;
+    if (nb < 1 || out_dim < 1 || in_dim < 16 || in_dim % 16 != 0) return Q4A_ERR_SHAPE;
+    if (nb > ((int64_t)1 << 31) - 1 || out_dim > (int64_t)1 << 30 || in_dim > (int64_t)1 << 24)
+        return Q4A_ERR_UNSUPPORTED;
+    if (!aligned(w, 16) || !aligned(x, 16) || !aligned(w_scale, 4) || !aligned(x_scale, 4)) return Q4A_ERR_ALIGN;
+    return Q4A_OK;
+}
+
+q4a_status check_gemm_fp8(const Fp8Gemm& g) {
+    if (!g.y) return Q4A_ERR_NULL;
+    if (!type_ok(g.y_type)) return Q4A_ERR_SHAPE;
+    const q4a_status st = check_fp8_product(g.w, g.w_scale, g.x, g.x_scale, g.nb, g.out_dim, g.in_dim);
+    if (st != Q4A_OK) return st;
+    return aligned(g.y, (uintptr_t)fp8_type_bytes(g.y_type)) ? Q4A_OK : Q4A_ERR_ALIGN;
+}
+
+q4a_status check_gate_up_fp8(const Fp8Gemm& g) {
+    if (!g.q || !g.scale) return Q4A_ERR_NULL;
+    if (g.out_dim < 16 || g.out_dim % 16 != 0) return Q4A_ERR_SHAPE;
+    const q4a_status st = check_fp8_product(g.w, g.w_scale, g.x, g.x_scale, g.nb, 2 * g.out_dim, g.in_dim);
+    if (st != Q4A_OK) return st;
+    if (g.out_dim % kFp8Block != 0) return Q4A_ERR_UNSUPPORTED;
+    return aligned(g.q, 16) && aligned(g.scale, 4) ? Q4A_OK : Q4A_ERR_ALIGN;
+}
+
+}  // namespace
+}  // namespace q4a
+
+extern "C" {
+
+q4a_status q4a_quantize_fp8(uint8_t* q, float* scale, const void* x, q4a_type x_type, int64_t nb, int64_t dim,
+                            q4a_stream_t stream) {
+    if (!x) return Q4A_ERR_NULL;
+    const q4a_status st = check_fp8_rows(q, scale, nb, dim);
+    if (st != Q4A_OK) return st;
+    if (!type_ok(x_type)) return Q4A_ERR_SHAPE;
+    if (!aligned(x, 16)) return Q4A_ERR_ALIGN;
+    Fp8Norm n = {};
+    n.q = q;
+    n.scale = scale;
+    n.x = x;
+    n.x_type = x_type;
+    n.nb = nb;
+    n.dim = dim;
+    return launch_fp8_rows(n, (cudaStream_t)stream);
+}
+
+q4a_status q4a_add_rmsnorm_fp8(uint8_t* q, float* scale, void* x_new, const void* x, q4a_type x_type,
+                               const void* residual, q4a_type res_type, const uint16_t* norm_w, float eps,
+                               float shift, int64_t nb, int64_t dim, q4a_stream_t stream) {
+    const Fp8Norm n = {q, scale, x_new, x, x_type, residual, res_type, norm_w, eps, shift, nb, dim};
+    const q4a_status st = check_add_rmsnorm(n);
+    return st != Q4A_OK ? st : launch_fp8_rows(n, (cudaStream_t)stream);
+}
+
+q4a_status q4a_dequant_fp8(uint8_t* w8, float* w_scale, const uint8_t* w, const uint16_t* s, const uint16_t* b,
+                           int64_t rows, int64_t in_dim, q4a_stream_t stream) {
+    if (!w8 || !w_scale || !w || !s || !b) return Q4A_ERR_NULL;
+    const q4a_status st = check_matrix_shape(rows, in_dim);
+    if (st != Q4A_OK) return st;
+    if (!aligned(w8, 16) || !aligned(w_scale, 4) || !aligned(w, 16) || !aligned(s, 2) || !aligned(b, 2))
+        return Q4A_ERR_ALIGN;
+    return launch_dequant_fp8(w8, w_scale, w, s, b, rows, in_dim, (cudaStream_t)stream);
+}
+
+q4a_status q4a_gemm_fp8(void* y, q4a_type y_type, const uint8_t* w, const float* w_scale, const uint8_t* x,
+                        const float* x_scale, int64_t nb, int64_t out_dim, int64_t in_dim, q4a_stream_t stream) {
+    const Fp8Gemm g = {y, y_type, nullptr, nullptr, w, w_scale, x, x_scale, nb, out_dim, in_dim};
+    const q4a_status st = check_gemm_fp8(g);
+    return st != Q4A_OK ? st : launch_gemm_fp8(g, (cudaStream_t)stream);
+}
+
+q4a_status q4a_gemm_fp8_gate_up_silu(uint8_t* q, float* scale, const uint8_t* w, const float* w_scale,
+                                     const uint8_t* x, const float* x_scale, int64_t nb, int64_t inter,
+                                     int64_t in_dim, q4a_stream_t stream) {
+    const Fp8Gemm g = {nullptr, Q4A_F32, q, scale, w, w_scale, x, x_scale, nb, inter, in_dim};
+    const q4a_status st = check_gate_up_fp8(g);
+    return st != Q4A_OK ? st : launch_gemm_fp8(g, (cudaStream_t)stream);
+}
+
+q4a_status q4a_mlp_fp8(void* y, q4a_type y_type, void* x_new, uint8_t* n, float* n_scale, uint8_t* h,
+                       float* h_scale, const void* x, q4a_type x_type, const void* residual, q4a_type res_type,
+                       const uint16_t* norm_w, float eps, float shift, const uint8_t* w_gu, const float* ws_gu,
+                       const uint8_t* w_dn, const float* ws_dn, int64_t nb, int64_t hidden, int64_t inter,
+                       q4a_stream_t stream) {
+    const Fp8Norm norm = {n, n_scale, x_new, x, x_type, residual, res_type, norm_w, eps, shift, nb, hidden};
+    const Fp8Gemm gu = {nullptr, Q4A_F32, h, h_scale, w_gu, ws_gu, n, n_scale, nb, inter, hidden};
+    const Fp8Gemm dn = {y, y_type, nullptr, nullptr, w_dn, ws_dn, h, h_scale, nb, hidden, inter};
+    q4a_status st = check_add_rmsnorm(norm);
+    if (st == Q4A_OK) st = check_gate_up_fp8(gu);
+    if (st == Q4A_OK) st = check_gemm_fp8(dn);
+    if (st == Q4A_OK) st = launch_fp8_rows(norm, (cudaStream_t)stream);
+    if (st == Q4A_OK) st = launch_gemm_fp8(gu, (cudaStream_t)stream);
+    if (st == Q4A_OK) st = launch_gemm_fp8(dn, (cudaStream_t)stream);
+    return st;
 }
 
 q4a_status q4a_check_device_error(q4a_stream_t stream) {

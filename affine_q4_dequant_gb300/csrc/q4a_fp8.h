@@ -1,0 +1,74 @@
+// q4a_fp8.h -- the 8-bit (e4m3, block-scaled) operators' launchers, called by the C ABI.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "q4a.h"
+
+namespace q4a {
+
+constexpr int kFp8Block = 128;                    // columns (and weight rows) of one scale
+constexpr int64_t kFp8MaxDim = 32768;             // longest row that q4a_quantize_fp8 and the norm take
+constexpr float kFp8Top = 448.0f;                 // the largest e4m3 value
+constexpr float kFp8Floor = 7.888609052210118e-31f;   // 2^-100: a block's smallest maximum, so that
+                                                  // neither its scale nor 1 / scale leaves fp32's normal range
+
+inline int64_t fp8_type_bytes(q4a_type t) { return t == Q4A_F32 ? 4 : 2; }
+
+// Rows of activations to 8 bits, with the RMSNorm before it when norm_w is set.
+struct Fp8Norm {
+    uint8_t* q;
+    float* scale;
+    void* x_new;
+    const void* x;
+    q4a_type x_type;
+    const void* residual;
+    q4a_type res_type;
+    const uint16_t* norm_w;
+    float eps, shift;
+    int64_t nb, dim;
+};
+q4a_status launch_fp8_rows(const Fp8Norm& n, cudaStream_t stream);
+
+// Packed 4-bit weights to 8-bit blocks.
+q4a_status launch_dequant_fp8(uint8_t* w8, float* w_scale, const uint8_t* w, const uint16_t* s, const uint16_t* b,
+                              int64_t rows, int64_t in_dim, cudaStream_t stream);
+
+// The block-scaled product: y, or with q set the gated form, whose w holds out_dim gate rows, then
+// out_dim up rows.
+struct Fp8Gemm {
+    void* y;
+    q4a_type y_type;
+    uint8_t* q;
+    float* scale;
+    const uint8_t* w;
+    const float* w_scale;
+    const uint8_t* x;
+    const float* x_scale;
+    int64_t nb, out_dim, in_dim;
+};
+q4a_status launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t stream);
+
+}  // namespace q4a
+
+#ifdef __CUDACC__
+namespace q4a {
+namespace {
+
+// Two values to e4m3 (round to nearest even; beyond +-448 clamps, NaN stays NaN), a in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+    return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
+}
+
+// A block's scale from its largest magnitude (fmaxf drops a NaN, so the scale is the other values').
+__device__ __forceinline__ float fp8_scale(float amax) { return fmaxf(amax, kFp8Floor) / kFp8Top; }
+
+}  // namespace
+}  // namespace q4a
+#endif

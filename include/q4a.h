@@ -59,6 +59,9 @@ typedef enum q4a_status {
     Q4A_ERR_TIMEOUT = 6      /* a kernel gave up a bounded wait (q4a_check_device_error) */
 } q4a_status;
 
+/* Element types of the buffers that the 8-bit entry points take in more than one type. */
+typedef enum q4a_type { Q4A_F32 = 0, Q4A_F16 = 1, Q4A_BF16 = 2 } q4a_type;
+
 /* Upper limits of the host-side schedule. */
 #define Q4A_MAX_SEGMENTS 512   /* routed-expert segments per q4a_gemv_experts call */
 
@@ -397,6 +400,115 @@ Q4A_API q4a_status q4a_moe_combine(float* out, const float* y, const int32_t* sl
                            int n_tok, int top_k, int64_t n_slots, int64_t hidden,
                            const float* y_shared, const uint16_t* gate, const float* x,
                            q4a_stream_t stream);
+
+/*
+ * The 8-bit form: activations and weights held as e4m3 codes (4 exponent bits, 3 mantissa bits,
+ * largest value 448) with fp32 scales, for batches wide enough that the product is a contraction
+ * and for decode steps on weights that are kept in 8 bits.
+ *   activations  q [nb][dim] with a scale for each run of 128 columns of a row,
+ *                scale [nb][ceil(dim/128)]
+ *   weights      w [out_dim][in_dim] with a scale for each block of 128 x 128,
+ *                w_scale [ceil(out_dim/128)][ceil(in_dim/128)]
+ *   The value is code * scale. Where this library writes scales, a block of values v gets
+ *       scale = max(max|v|, 2^-100) / 448,   code = e4m3(v * (1 / scale)), round to nearest even,
+ *   in fp32; a block of zeros has scale 2^-100 / 448 and zero codes. The scales that a product
+ *   reads are any fp32 values. The last block of a row or column may be short. A NaN becomes a
+ *   NaN code and leaves its block's scale to the other values; an infinity makes its block's
+ *   scale infinite: either comes out of a product as NaN.
+ *   Rows are multiples of 16 bytes: dim, in_dim and inter are multiples of 16 (the products fetch
+ *   them with tensor copies).
+ *
+ * q4a_quantize_fp8 -- activations in 8 bits.
+ *   q      out  e4m3 [nb][dim]
+ *   scale  out  fp32 [nb][ceil(dim/128)]
+ *   x      in   x_type [nb][dim]
+ *   Requires nb >= 1, dim >= 16, dim % 16 == 0; dim <= 32768 (else Q4A_ERR_UNSUPPORTED); q and x
+ *   16-byte aligned, scale 4-byte aligned.
+ */
+Q4A_API q4a_status q4a_quantize_fp8(uint8_t* q, float* scale, const void* x, q4a_type x_type, int64_t nb,
+                                    int64_t dim, q4a_stream_t stream);
+
+/*
+ * q4a_add_rmsnorm_fp8 -- the residual's addition and the RMSNorm in one pass, with an 8-bit
+ * output: the step before every product of a layer ("BATCH_MSL", hyperconnection.metal
+ * fn_group_norm_b, one normalisation group).
+ *     x'[r][i] = residual type( x[r][i] + residual[r][i] )      (x itself without a residual)
+ *     n[r][i]  = x'[r][i] * (mean_i x'[r][i]^2 + eps)^(-1/2) * (norm_w[i] + shift),  in 8 bits
+ *   The sum is rounded to fp32, then to the residual's type; the norm reads the stored value.
+ *   q, scale   out  as q4a_quantize_fp8
+ *   x_new      out  res_type [nb][dim], x'; may be NULL, the same buffer as residual (in place)
+ *                   or, with x_type == res_type, as x. Any other overlap is Q4A_ERR_SHAPE, and so
+ *                   is x_new without a residual.
+ *   x          in   x_type [nb][dim], the layer's output
+ *   residual   in   res_type [nb][dim] or NULL
+ *   norm_w     in   bf16 [dim]
+ *   Requires eps >= 0 and the sizes of q4a_quantize_fp8; q, x_new, x, residual and norm_w 16-byte
+ *   aligned, scale 4-byte aligned.
+ */
+Q4A_API q4a_status q4a_add_rmsnorm_fp8(uint8_t* q, float* scale, void* x_new, const void* x, q4a_type x_type,
+                                       const void* residual, q4a_type res_type, const uint16_t* norm_w, float eps,
+                                       float shift, int64_t nb, int64_t dim, q4a_stream_t stream);
+
+/*
+ * q4a_dequant_fp8 -- packed 4-bit weights laid out in 8 bits, once, for the products below:
+ * W = s*q + b in fp32 (one fused multiply-add), in e4m3 blocks.
+ *   w8       out  e4m3 [rows][in_dim]
+ *   w_scale  out  fp32 [ceil(rows/128)][ceil(in_dim/128)]
+ *   w, s, b  in   as q4a_gemv
+ *   Requires the shapes of q4a_gemv; w8 and w 16-byte aligned, s and b 2-byte, w_scale 4-byte.
+ */
+Q4A_API q4a_status q4a_dequant_fp8(uint8_t* w8, float* w_scale, const uint8_t* w, const uint16_t* s,
+                                   const uint16_t* b, int64_t rows, int64_t in_dim, q4a_stream_t stream);
+
+/*
+ * q4a_gemm_fp8 -- y = W.x on block-scaled 8-bit operands:
+ *     y[r][o] = sum_k x_scale[r][k] * w_scale[o/128][k] * sum_{i in block k} x[r][i] * w[o][i]
+ *   Products and sums of codes on the tensor cores, scales and the sum over blocks in fp32.
+ *   y                 out  y_type [nb][out_dim], rounded once
+ *   w, w_scale        in   e4m3 weights and their scales
+ *   x, x_scale        in   e4m3 activations and their scales
+ *   Requires nb >= 1, out_dim >= 1 (odd included), in_dim >= 16, in_dim % 16 == 0;
+ *   out_dim <= 2^30, in_dim <= 2^24, nb < 2^31 (else Q4A_ERR_UNSUPPORTED); w and x 16-byte
+ *   aligned, y aligned to its element, scales 4-byte aligned.
+ */
+Q4A_API q4a_status q4a_gemm_fp8(void* y, q4a_type y_type, const uint8_t* w, const float* w_scale, const uint8_t* x,
+                                const float* x_scale, int64_t nb, int64_t out_dim, int64_t in_dim,
+                                q4a_stream_t stream);
+
+/*
+ * q4a_gemm_fp8_gate_up_silu -- the gate and up projections in 8 bits with the activation in the
+ * epilogue and an 8-bit output, the down product's input ("BATCH_MSL", experts.metal
+ * fn_moe_gate_up_b followed by fn_moe_act_b):
+ *     h[r][o] = silu(g) * u,  g = (W_gate.x)[r][o],  u = (W_up.x)[r][o],  silu(v) = v / (1 + e^-v)
+ *   g, u and h in fp32; no wider h exists.
+ *   q        out  e4m3 [nb][inter]
+ *   scale    out  fp32 [nb][inter/128]
+ *   w        in   e4m3 [2*inter][in_dim]: gate rows, then up rows; w_scale [2*inter/128][ceil(in_dim/128)]
+ *   Requires inter % 16 == 0 (else Q4A_ERR_SHAPE) and inter % 128 == 0 (else Q4A_ERR_UNSUPPORTED:
+ *   the gate's and the up rows' scale blocks would not match); q 16-byte aligned, scale 4-byte;
+ *   everything else as q4a_gemm_fp8.
+ */
+Q4A_API q4a_status q4a_gemm_fp8_gate_up_silu(uint8_t* q, float* scale, const uint8_t* w, const float* w_scale,
+                                             const uint8_t* x, const float* x_scale, int64_t nb, int64_t inter,
+                                             int64_t in_dim, q4a_stream_t stream);
+
+/*
+ * q4a_mlp_fp8 -- a layer's gated MLP on 8-bit operands, the sister of q4a_decode_mlp for wide
+ * batches: q4a_add_rmsnorm_fp8, q4a_gemm_fp8_gate_up_silu, then q4a_gemm_fp8 of the down
+ * projection, the same results as the three calls.
+ *   y                   out  y_type [nb][hidden]
+ *   x_new               out  as q4a_add_rmsnorm_fp8 (may be NULL)
+ *   n, n_scale          out  e4m3 [nb][hidden], fp32 [nb][ceil(hidden/128)]: the normalised rows
+ *   h, h_scale          out  e4m3 [nb][inter], fp32 [nb][inter/128]: the down projection's input
+ *   w_gu, ws_gu         in   [2*inter][hidden] and its scales, gate rows, then up rows
+ *   w_dn, ws_dn         in   [hidden][inter] and its scales
+ *   Every argument is checked before anything is launched.
+ */
+Q4A_API q4a_status q4a_mlp_fp8(void* y, q4a_type y_type, void* x_new, uint8_t* n, float* n_scale, uint8_t* h,
+                               float* h_scale, const void* x, q4a_type x_type, const void* residual,
+                               q4a_type res_type, const uint16_t* norm_w, float eps, float shift,
+                               const uint8_t* w_gu, const float* ws_gu, const uint8_t* w_dn, const float* ws_dn,
+                               int64_t nb, int64_t hidden, int64_t inter, q4a_stream_t stream);
 
 /*
  * q4a_gemv_kernel_choice -- which kernel q4a_gemv (and q4a_gemv_silu) would launch for these

@@ -68,6 +68,11 @@ def _load():
             "q4o_experts_lowbit": (None, [P, P, P, P, P, P, P, P, P, P, P, I, I, I, I]),
             "q4o_gemv_f32x": (None, [P, P, P, P, P, P, I, I, I]),
             "q4o_quantize": (None, [P, P, P, P, I, I]),
+            "q4o_e4m3_value": (D, [ctypes.c_uint8]),
+            "q4o_e4m3_round": (ctypes.c_uint8, [D]),
+            "q4o_e4m3_scales": (None, [P, P, I, I, I]),
+            "q4o_add_rmsnorm": (None, [P, P, P, I, P, I, P, D, D, I, I]),
+            "q4o_gemm_e4m3": (None, [P, P, P, P, P, P, I, I, I]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -373,3 +378,52 @@ def quantize(w_f32):
     _load().q4o_quantize(_p(packed), _p(s), _p(b), _p(w), rows, in_dim)
     return packed, s, b
 
+
+
+# ---- the 8-bit form ---------------------------------------------------------------------------
+
+_TYPE = {np.dtype(np.float32): 0, np.dtype(np.float16): 1, np.dtype(np.uint16): 2}   # uint16: bfloat16 bits
+
+
+def e4m3_value(code: int) -> float:
+    return _load().q4o_e4m3_value(code)
+
+
+def e4m3_round(v: float) -> int:
+    return _load().q4o_e4m3_round(v)
+
+
+def e4m3_values(codes) -> np.ndarray:
+    """The codes' values in float64."""
+    return np.array([e4m3_value(c) for c in range(256)])[np.asarray(codes, np.uint8)]
+
+
+def e4m3_scales(v, block_rows: int = 1) -> np.ndarray:
+    """max(max|v|, 2^-100) / 448 per block of block_rows x 128, in float64."""
+    v = _c(v, np.float64)
+    rows, cols = v.shape
+    scale = np.empty((-(-rows // block_rows), -(-cols // 128)), np.float64)
+    _load().q4o_e4m3_scales(_p(scale), _p(v), rows, cols, block_rows)
+    return scale
+
+
+def add_rmsnorm(x, residual=None, norm_w=None, eps: float = 1e-6, shift: float = 0.0):
+    """(n, x_new) in float64 before the 8-bit rounding ([BATCH_MSL] fn_group_norm_b, one group);
+    x and residual are float32, float16 or bfloat16-bit (uint16) arrays; without norm_w n is x_new."""
+    x = np.ascontiguousarray(x)
+    nb, dim = x.shape
+    r = None if residual is None else np.ascontiguousarray(residual)
+    n, x_new = np.empty((nb, dim), np.float64), np.empty((nb, dim), np.float64)
+    _load().q4o_add_rmsnorm(_p(n), _p(x_new), _p(x), _TYPE[x.dtype], _p(r), 0 if r is None else _TYPE[r.dtype],
+                            _p(None if norm_w is None else _c(norm_w, np.uint16)), eps, shift, nb, dim)
+    return n, x_new
+
+
+def gemm_e4m3(w, w_scale, x, x_scale):
+    """(y, mag): W x on e4m3 codes with their block scales, and the sum of magnitudes, in float64."""
+    w, ws, x, xs = _c(w, np.uint8), _c(w_scale, np.float32), _c(x, np.uint8), _c(x_scale, np.float32)
+    nb, in_dim = x.shape
+    out_dim = w.shape[0]
+    y, mag = np.empty((nb, out_dim), np.float64), np.empty((nb, out_dim), np.float64)
+    _load().q4o_gemm_e4m3(_p(y), _p(mag), _p(w), _p(ws), _p(x), _p(xs), nb, out_dim, in_dim)
+    return y, mag

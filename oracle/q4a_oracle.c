@@ -768,3 +768,115 @@ Q4O_EXPORT void q4o_quantize(uint8_t* packed, uint16_t* s, uint16_t* b, const fl
     }
     free(codes);
 }
+
+/* ---- the 8-bit form: e4m3 codes with a scale per 128 columns, or per 128 x 128 block -------- */
+
+/* The value of an e4m3 code: sign, 4 exponent bits (bias 7), 3 mantissa bits; exponent 0 is
+ * subnormal, 0x7F and 0xFF are NaN, there is no infinity. */
+Q4O_EXPORT double q4o_e4m3_value(uint8_t c)
+{
+    const int e = (c >> 3) & 15, m = c & 7;
+    if ((c & 0x7F) == 0x7F)
+        return NAN;
+    const double v = e == 0 ? ldexp((double)m, -9) : ldexp(8.0 + (double)m, e - 10);
+    return c & 0x80 ? -v : v;
+}
+
+/* The e4m3 code nearest to v, ties to the even mantissa; beyond 448 it clamps, NaN gives 0x7F.
+ * Found by comparing with every code's value. */
+Q4O_EXPORT uint8_t q4o_e4m3_round(double v)
+{
+    if (isnan(v))
+        return 0x7F;
+    const uint8_t sign = signbit(v) ? 0x80 : 0;
+    const double a = fabs(v);
+    int best = 0;
+    for (int c = 1; c < 0x7F; c++) {
+        const double d = fabs(q4o_e4m3_value((uint8_t)c) - a), b = fabs(q4o_e4m3_value((uint8_t)best) - a);
+        if (d < b || (d == b && (c & 1) == 0))
+            best = c;
+    }
+    return (uint8_t)(sign | best);
+}
+
+/* scale[i][j] = max(max |v| over the block, 2^-100) / 448 for blocks of br rows x 128 columns;
+ * a NaN counts as nothing. */
+Q4O_EXPORT void q4o_e4m3_scales(double* scale, const double* v, int64_t rows, int64_t cols, int64_t br)
+{
+    const int64_t nk = (cols + 127) / 128;
+    for (int64_t i = 0; i < (rows + br - 1) / br; i++)
+        for (int64_t j = 0; j < nk; j++) {
+            double top = ldexp(1.0, -100);
+            for (int64_t r = i * br; r < (i + 1) * br && r < rows; r++)
+                for (int64_t c = j * 128; c < (j + 1) * 128 && c < cols; c++)
+                    if (fabs(v[r * cols + c]) > top)
+                        top = fabs(v[r * cols + c]);
+            scale[i * nk + j] = top / 448.0;
+        }
+}
+
+/* Element i of a buffer of type 0 (binary32), 1 (binary16) or 2 (bfloat16). */
+static double typed_value(const void* p, int64_t type, int64_t i)
+{
+    if (type == 0)
+        return (double)((const float*)p)[i];
+    return type == 1 ? half_value(((const uint16_t*)p)[i]) : bf16_value(((const uint16_t*)p)[i]);
+}
+
+/* The residual's addition and the RMSNorm ([BATCH_MSL] fn_group_norm_b, one group), before the
+ * 8-bit rounding: x_new = T(float(x + residual)) as values, n = x_new / sqrt(mean x_new^2 + eps)
+ * * (w + shift). residual may be NULL (x_new = x then); norm_w NULL leaves n = x_new. */
+Q4O_EXPORT void q4o_add_rmsnorm(double* n, double* x_new, const void* x, int64_t x_type, const void* residual,
+                                int64_t res_type, const uint16_t* norm_w, double eps, double shift, int64_t nb,
+                                int64_t dim)
+{
+    for (int64_t r = 0; r < nb; r++) {
+        double ssq = 0.0;
+        for (int64_t i = 0; i < dim; i++) {
+            double v = typed_value(x, x_type, r * dim + i);
+            if (residual) {
+                const float f = (float)(v + typed_value(residual, res_type, r * dim + i));
+                v = res_type == 0 ? (double)f : res_type == 1 ? half_value(half_round((double)f))
+                                                              : bf16_value(bf16_round(f));
+            }
+            x_new[r * dim + i] = v;
+            ssq += v * v;
+        }
+        const double root = sqrt(ssq / (double)dim + eps);
+        for (int64_t i = 0; i < dim; i++)
+            n[r * dim + i] = norm_w ? x_new[r * dim + i] / root * (bf16_value(norm_w[i]) + shift)
+                                    : x_new[r * dim + i];
+    }
+}
+
+/* y[r][o] = sum_i (w[o][i] ws[o/128][i/128]) (x[r][i] xs[r][i/128]) from e4m3 codes, every
+ * operand's value formed first; mag is the same sum of magnitudes. */
+Q4O_EXPORT void q4o_gemm_e4m3(double* y, double* mag, const uint8_t* w, const float* ws, const uint8_t* x,
+                              const float* xs, int64_t nb, int64_t out_dim, int64_t in_dim)
+{
+    const int64_t nk = (in_dim + 127) / 128;
+    double table[256];
+    for (int c = 0; c < 256; c++)
+        table[c] = q4o_e4m3_value((uint8_t)c);
+    double* xv = (double*)malloc((size_t)(nb * in_dim) * sizeof(double));
+    double* wv = (double*)malloc((size_t)in_dim * sizeof(double));
+    for (int64_t r = 0; r < nb; r++)
+        for (int64_t i = 0; i < in_dim; i++)
+            xv[r * in_dim + i] = table[x[r * in_dim + i]] * (double)xs[r * nk + i / 128];
+    for (int64_t o = 0; o < out_dim; o++) {
+        for (int64_t i = 0; i < in_dim; i++)
+            wv[i] = table[w[o * in_dim + i]] * (double)ws[o / 128 * nk + i / 128];
+        for (int64_t r = 0; r < nb; r++) {
+            double acc = 0.0, m = 0.0;
+            for (int64_t i = 0; i < in_dim; i++) {
+                const double p = wv[i] * xv[r * in_dim + i];
+                acc += p;
+                m += fabs(p);
+            }
+            y[r * out_dim + o] = acc;
+            mag[r * out_dim + o] = m;
+        }
+    }
+    free(wv);
+    free(xv);
+}

@@ -1,0 +1,151 @@
+"""Refusals of the 8-bit entry points, on the host: by the C ABI with its status codes and by the
+binding before a pointer leaves it."""
+
+import ctypes
+
+import pytest
+
+OK, NULL, SHAPE, ALIGN, UNSUP, CUDA, TIMEOUT = range(7)
+F32, F16, BF16 = 0, 1, 2
+A = 0x100000
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import __graft_entry__
+
+    lib = ctypes.CDLL(__graft_entry__._build_module().build())
+    P, I64, I32, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+    lib.q4a_quantize_fp8.argtypes = [P, P, P, I32, I64, I64, P]
+    lib.q4a_add_rmsnorm_fp8.argtypes = [P, P, P, P, I32, P, I32, P, F, F, I64, I64, P]
+    lib.q4a_dequant_fp8.argtypes = [P, P, P, P, P, I64, I64, P]
+    lib.q4a_gemm_fp8.argtypes = [P, I32, P, P, P, P, I64, I64, I64, P]
+    lib.q4a_gemm_fp8_gate_up_silu.argtypes = [P, P, P, P, P, P, I64, I64, I64, P]
+    lib.q4a_mlp_fp8.argtypes = [P, I32, P, P, P, P, P, P, I32, P, I32, P, F, F, P, P, P, P, I64, I64, I64, P]
+    return lib
+
+
+def test_quantize_refusals(lib):
+    def call(q=A, s=A, x=A, t=F32, nb=2, dim=64):
+        return lib.q4a_quantize_fp8(q, s, x, t, nb, dim, None)
+
+    assert call(q=None) == call(s=None) == call(x=None) == NULL
+    assert call(nb=0) == call(dim=0) == call(dim=24) == call(nb=-1) == call(t=3) == call(t=-1) == SHAPE
+    assert call(dim=32784) == call(nb=1 << 31) == UNSUP
+    assert call(q=A + 8) == call(x=A + 4) == call(s=A + 2) == ALIGN
+
+
+def test_add_rmsnorm_refusals(lib):
+    big = 1 << 20
+
+    def call(q=A, s=A, xn=5 * big, x=big, xt=F32, r=9 * big, rt=F32, w=A, eps=1e-6, nb=2, dim=64):
+        return lib.q4a_add_rmsnorm_fp8(q, s, xn, x, xt, r, rt, w, eps, 0.0, nb, dim, None)
+
+    assert call(q=None) == call(s=None) == call(x=None) == call(w=None) == NULL
+    assert call(nb=0) == call(dim=40) == call(eps=-1.0) == call(eps=NAN) == call(xt=3) == call(rt=7) == SHAPE
+    assert call(r=None) == SHAPE                       # x_new without a residual
+    assert call(xn=9 * big + 16) == SHAPE              # x_new shifted against the residual
+    assert call(xn=big + 256) == SHAPE                 # x_new overlapping x
+    assert call(xn=big, xt=F16) == SHAPE               # x_new on x of another type
+    assert call(dim=32784) == UNSUP
+    assert call(x=big + 8) == call(r=9 * big + 4) == call(w=A + 2) == call(xn=5 * big + 8) == ALIGN
+
+
+def test_dequant_refusals(lib):
+    def call(o=A, os=A, w=A, s=A, b=A, rows=8, ind=128):
+        return lib.q4a_dequant_fp8(o, os, w, s, b, rows, ind, None)
+
+    assert call(o=None) == call(os=None) == call(w=None) == call(s=None) == call(b=None) == NULL
+    assert call(rows=0) == call(ind=96) == call(ind=0) == SHAPE
+    assert call(rows=(1 << 30) + 1) == UNSUP
+    assert call(o=A + 8) == call(w=A + 8) == call(s=A + 1) == call(os=A + 2) == ALIGN
+
+
+def test_gemm_refusals(lib):
+    def call(y=A, t=F32, w=A, ws=A, x=A, xs=A, nb=2, out=8, ind=64):
+        return lib.q4a_gemm_fp8(y, t, w, ws, x, xs, nb, out, ind, None)
+
+    assert call(y=None) == call(w=None) == call(ws=None) == call(x=None) == call(xs=None) == NULL
+    assert call(nb=0) == call(out=0) == call(ind=0) == call(ind=40) == call(t=3) == SHAPE
+    assert call(nb=1 << 31) == call(out=(1 << 30) + 1) == call(ind=(1 << 24) + 16) == UNSUP
+    assert call(w=A + 8) == call(x=A + 8) == call(y=A + 2) == call(xs=A + 2) == call(ws=A + 1) == ALIGN
+    assert call(y=A + 1, t=BF16) == ALIGN
+
+
+def test_gate_up_refusals(lib):
+    def call(q=A, s=A, w=A, ws=A, x=A, xs=A, nb=2, inter=128, ind=64):
+        return lib.q4a_gemm_fp8_gate_up_silu(q, s, w, ws, x, xs, nb, inter, ind, None)
+
+    assert call(q=None) == call(s=None) == call(w=None) == call(xs=None) == NULL
+    assert call(nb=0) == call(inter=0) == call(inter=120) == call(ind=24) == SHAPE
+    assert call(inter=192) == call(inter=64) == UNSUP
+    assert call(q=A + 8) == call(s=A + 2) == call(w=A + 4) == ALIGN
+
+
+def test_mlp_refusals(lib):
+    big = 1 << 20
+
+    def call(y=A, t=F32, xn=None, n=A, ns=A, h=A, hs=A, x=big, xt=F32, r=None, rt=F32, nw=A, eps=1e-6, wg=A, sg=A,
+             wd=A, sd=A, nb=2, hidden=64, inter=128):
+        return lib.q4a_mlp_fp8(y, t, xn, n, ns, h, hs, x, xt, r, rt, nw, eps, 0.0, wg, sg, wd, sd, nb, hidden, inter,
+                               None)
+
+    for k in ("y", "n", "ns", "h", "hs", "x", "nw", "wg", "sg", "wd", "sd"):
+        assert call(**{k: None}) == NULL, k
+    assert call(nb=0) == call(hidden=72) == call(inter=8) == call(eps=-1.0) == call(t=5) == SHAPE
+    assert call(inter=192) == UNSUP
+    assert call(xn=A) == SHAPE
+    assert call(wd=A + 8) == call(h=A + 8) == ALIGN
+
+
+@pytest.fixture(scope="module")
+def q4a():
+    import __graft_entry__
+
+    __graft_entry__._build_module().build()
+    torch = pytest.importorskip("torch")
+    import affine_q4_dequant_gb300
+
+    return affine_q4_dequant_gb300, torch
+
+
+def _bad(call, match, kind=ValueError):
+    with pytest.raises(kind, match=match):
+        call()
+
+
+def test_binding_refusals(q4a):
+    mod, torch = q4a
+    f8, f32, bf = torch.float8_e4m3fn, torch.float32, torch.bfloat16
+    x = torch.zeros(2, 272, dtype=f32)
+    nw = torch.zeros(272, dtype=bf)
+    _bad(lambda: mod.quantize_fp8(x, q=torch.zeros(2, 256, dtype=f8)), "q: shape")
+    _bad(lambda: mod.quantize_fp8(x, scale=torch.zeros(2, 2, dtype=f32)), "scale: shape")
+    _bad(lambda: mod.quantize_fp8(x.double()), "x: dtype", TypeError)
+    _bad(lambda: mod.quantize_fp8(x), "CUDA", TypeError)
+    _bad(lambda: mod.quantize_fp8(x[0]), "dimensions")
+    _bad(lambda: mod.add_rmsnorm_fp8(x, nw[:256]), "norm_w: shape")
+    _bad(lambda: mod.add_rmsnorm_fp8(x, nw, residual=torch.zeros(3, 272)), "residual: shape")
+    _bad(lambda: mod.add_rmsnorm_fp8(x, nw, x_new=x), "needs a residual")
+    _bad(lambda: mod.add_rmsnorm_fp8(x, nw, residual=x, x_new=torch.zeros(2, 256)), "x_new: shape")
+    _bad(lambda: mod.add_rmsnorm_fp8(x, nw, residual=x.double()), "residual: dtype", TypeError)
+    w, ws = torch.zeros(130, 272, dtype=f8), torch.zeros(2, 3)
+    xq, xs = torch.zeros(2, 272, dtype=f8), torch.zeros(2, 3)
+    _bad(lambda: mod.gemm_fp8(w, ws[:1], xq, xs), "w_scale: shape")
+    _bad(lambda: mod.gemm_fp8(w[:, :256], ws, xq, xs), "w: shape")
+    _bad(lambda: mod.gemm_fp8(w, ws, xq, xs[:, :2]), "x_scale: shape")
+    _bad(lambda: mod.gemm_fp8(w, ws, xq, xs, out=torch.zeros(2, 131)), "y: shape")
+    _bad(lambda: mod.gemm_fp8(w, ws, xq, xs, out_dtype=torch.float64), "y: dtype", TypeError)
+    _bad(lambda: mod.gemm_fp8(w, ws, xq, xs), "CUDA", TypeError)
+    g, gs = torch.zeros(256, 272, dtype=f8), torch.zeros(2, 3)
+    _bad(lambda: mod.gemm_fp8_gate_up_silu(g[:255], gs, xq, xs), "w: shape")
+    _bad(lambda: mod.gemm_fp8_gate_up_silu(g, gs, xq, xs, q=torch.zeros(2, 256, dtype=f8)), "q: shape")
+    _bad(lambda: mod.dequant_fp8(torch.zeros(8, 64, dtype=torch.uint8), torch.zeros(8, 1, dtype=bf),
+                                 torch.zeros(8, 2, dtype=bf)), "s: shape")
+    d, ds = torch.zeros(272, 128, dtype=f8), torch.zeros(3, 1)
+    _bad(lambda: mod.mlp_fp8(x, nw, g, gs, d[:, :112], ds), "w_dn: shape")
+    _bad(lambda: mod.mlp_fp8(x, nw, g, gs, d, ds, out=torch.zeros(2, 128)), "y: shape")
+    _bad(lambda: mod.mlp_fp8(x, nw, g, gs, d, ds, h=(torch.zeros(2, 64, dtype=f8), None)), "h: shape")
+    _bad(lambda: mod.mlp_fp8(x, nw, g, gs, d, ds, x_new=x), "needs a residual")
+    _bad(lambda: mod.mlp_fp8(x, nw, g, gs, d, ds), "CUDA", TypeError)

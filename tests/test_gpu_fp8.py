@@ -1,0 +1,475 @@
+"""GPU parity of the 8-bit operators (e4m3 codes with block scales) against the CPU oracle.
+
+Bars, from the arithmetic:
+* codes: rounding to e4m3 is off by at most half a step of the code's binade,
+  2^(max(floor(log2 |v / scale|), -6) - 4) times the scale, beside the relative error of the fp32
+  value that was rounded;
+* quantize_fp8: that value is x * (1 / scale) with three roundings, and a scale has one: 2^-24 each;
+* the norm: at most 64 + 37 additions and products of non-negative terms in the sum of squares
+  (each 2^-24 relative, halved by the root), then at most 8 roundings: 60 * 2^-24;
+* the product: a block's 128 exact products are added in fp32, truncating at worst (2^-23 of the
+  magnitudes each), then a rounded scale product and one fused multiply-add per block:
+  (128 * 2^-23 + (blocks + 2) * 2^-24) * sum |x w|, and the output's rounding;
+* the gated product: with those bounds eg, eu on g and u,
+  |dh| <= 1.1 (|u| + eu) eg + (|silu(g)| + 1.1 eg) eu + 2^-20 |h|  (silu' <= 1.1; expf, the
+  quotient and the product are a few roundings).
+"""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import affine_q4_dequant_gb300 as q4a  # noqa: E402
+import oracle  # noqa: E402
+import q4a_workloads as wl  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+F8 = torch.float8_e4m3fn
+U = 2.0 ** -24
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+HALF_STEP = {"f32": 2.0 ** -24, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}
+TINY = {"f32": 1e-45, "f16": 2.0 ** -25, "bf16": 1e-40}
+NORM_TOL = 60 * U
+
+
+def values(rng, shape, std=1.0):
+    """Activations whose columns differ in size, with outliers."""
+    v = rng.normal(0, std, shape) * np.exp(0.5 * rng.normal(0, 1, shape[1]))
+    v[:, ::97] *= 30.0
+    return v.astype(np.float32)
+
+
+def typed(v, t):
+    """(device tensor, host array for the oracle) of values in type t."""
+    d = torch.from_numpy(np.ascontiguousarray(v)).to(DEV).to(TYPES[t])
+    h = d.cpu()
+    return d, (h.view(torch.int16).numpy().view(np.uint16) if t == "bf16" else h.numpy())
+
+
+def host64(t):
+    return t.detach().cpu().to(torch.float64).numpy()
+
+
+def half_step(u):
+    """Half a step of the e4m3 binade that holds u (in units of the scale)."""
+    e = np.floor(np.log2(np.maximum(np.abs(u), 2.0 ** -40)))
+    return 2.0 ** (np.maximum(e, -6) - 4)
+
+
+def check_codes(q, scale, v, what, block_rows=1, err=0.0, rel=0.0, scale_tol=2 * U):
+    """q, scale (device tensors) against the float64 values v that they hold: err is what the value
+    may be off by before it is rounded, rel the same relative to it."""
+    rows, cols = v.shape
+    s_ref, s = oracle.e4m3_scales(v, block_rows), host64(scale)
+    assert s.shape == s_ref.shape, what
+    # the block's largest value is off by no more than the largest err of the block
+    e = np.broadcast_to(np.asarray(err, np.float64), v.shape)
+    slack = oracle.e4m3_scales(e, block_rows) if np.any(e) else 0.0
+    d = np.abs(s - s_ref) / ((scale_tol + rel) * s_ref + slack)
+    assert d.max() <= 1.0, f"{what}: scale off by {d.max():.3g} of the bound"
+    sv = np.repeat(np.repeat(s, block_rows, 0)[:rows], 128, 1)[:, :cols]
+    got = oracle.e4m3_values(q.view(torch.uint8).cpu().numpy()) * sv
+    bound = half_step(np.abs(v / sv) * (1 + 1e-6)) * sv + (rel + 4 * U) * np.abs(v) + e
+    ratio = np.abs(got - v) / bound
+    assert np.isfinite(got).all(), f"{what}: non-finite values"
+    assert ratio.max() <= 1.0, f"{what}: a code is off by {ratio.max():.3g} of the bound"
+
+
+def guarded(shape, dtype, fill):
+    """A buffer with 4 more rows, and the view of the first shape[0] rows."""
+    big = torch.full((shape[0] + 4,) + tuple(shape[1:]), fill, dtype=torch.float32, device=DEV).to(dtype)
+    return big, big[: shape[0]]
+
+
+def bits(t):
+    return t.contiguous().view(torch.uint8).cpu()
+
+
+def check_guard(big, n, what):
+    """The rows behind the last are as they were."""
+    rest = bits(big[n:])
+    same = bits(big[-1:]).reshape(-1)
+    assert torch.equal(rest.reshape(-1, same.numel()), same.expand(rest.reshape(-1, same.numel()).shape)), what
+
+
+# ---- rows ---------------------------------------------------------------------------------------
+
+ROWS = [(1, 16), (5, 64), (3, 128), (9, 144), (1, 640), (7, 656), (300, 512), (2, 4096), (33, 2064), (3, 8208),
+        (2, 16384), (3, 16400), (1, 32768)]
+
+
+@pytest.mark.parametrize("t", sorted(TYPES))
+@pytest.mark.parametrize("nb,dim", ROWS)
+def test_quantize(nb, dim, t):
+    x, xh = typed(values(np.random.default_rng(nb + dim), (nb, dim)), t)
+    bq, q = guarded((nb, dim), F8, 2.0)
+    bs, s = guarded((nb, -(-dim // 128)), torch.float32, 3.0)
+    q4a.quantize_fp8(x, q=q, scale=s)
+    check_codes(q, s, oracle.add_rmsnorm(xh)[0], f"quantize {nb}x{dim} {t}")
+    check_guard(bq, nb, "codes behind the last row")
+    check_guard(bs, nb, "scales behind the last row")
+
+
+@pytest.mark.parametrize("t,rt", [("f32", None), ("f16", None), ("bf16", None), ("f32", "f32"), ("f32", "bf16"),
+                                  ("f32", "f16"), ("f16", "f32"), ("f16", "f16"), ("f16", "bf16"), ("bf16", "f32"),
+                                  ("bf16", "f16"), ("bf16", "bf16")])
+@pytest.mark.parametrize("nb,dim", ROWS)
+def test_add_rmsnorm(nb, dim, t, rt):
+    rng = np.random.default_rng(3 * nb + dim)
+    x, xh = typed(values(rng, (nb, dim), 0.5), t)
+    w = wl.f32_to_bf16_bits(1 + 0.05 * rng.normal(0, 1, dim))
+    wd = torch.from_numpy(w.view(np.int16)).to(DEV)
+    r = rh = None
+    if rt is not None:
+        r, rh = typed(values(rng, (nb, dim), 2.0), rt)
+    q, s, x_new = q4a.add_rmsnorm_fp8(x, wd, residual=r, eps=1e-5, shift=0.5)
+    n, stored = oracle.add_rmsnorm(xh, rh, w, eps=1e-5, shift=0.5)
+    check_codes(q, s, n, f"norm {nb}x{dim} {t} + {rt}", rel=NORM_TOL)
+    if rt is None:
+        assert x_new is None
+    else:
+        assert x_new.dtype == TYPES[rt] and np.array_equal(host64(x_new), stored)
+        # in place on the residual, and without x_new: the same codes
+        r2 = r.clone()
+        q2, s2, same = q4a.add_rmsnorm_fp8(x, wd, residual=r2, eps=1e-5, shift=0.5, x_new=r2)
+        assert same is r2 and np.array_equal(host64(r2), stored)
+        q3, s3, none = q4a.add_rmsnorm_fp8(x, wd, residual=r, eps=1e-5, shift=0.5, want_x_new=False)
+        assert none is None
+        for a, b in ((q, q2), (s, s2), (q, q3), (s, s3)):
+            assert torch.equal(bits(a), bits(b))
+
+
+def test_rows_special_values():
+    v = np.random.default_rng(9).normal(0, 1, (8, 384)).astype(np.float32)
+    v[0] = 0.0                       # nothing: zero codes, the smallest scale
+    v[1, 128:256] = 0.0
+    v[2, 5] = np.nan                 # a NaN stays in its place
+    v[3, 200] = np.inf               # an infinite scale
+    v[4] *= 1e-36                    # below the smallest scale's reach
+    v[5] *= 1e34
+    v[6, :128] = -0.0
+    x = torch.from_numpy(v).to(DEV)
+    q, s = q4a.quantize_fp8(x)
+    qv, sv = oracle.e4m3_values(q.view(torch.uint8).cpu().numpy()), host64(s)
+    floor = np.float32(2.0 ** -100) / np.float32(448)
+    assert (qv[0] == 0).all() and (sv[0] == floor).all()
+    assert (qv[1, 128:256] == 0).all() and sv[1, 1] == floor
+    assert np.isnan(qv[2, 5]) and np.isfinite(np.delete(qv[2], 5)).all()
+    assert np.isinf(sv[3, 1]) and np.isnan(qv[3, 200])
+    assert (sv[4] == floor).all() and np.isfinite(qv[4]).all()
+    keep = [0, 1, 4, 5, 6, 7]
+    check_codes(q[keep], s[keep], v[keep].astype(np.float64), "special values")
+    w = torch.ones(384, dtype=torch.bfloat16, device=DEV)
+    q, s, _ = q4a.add_rmsnorm_fp8(x, w, eps=0.0)
+    qv = oracle.e4m3_values(q.view(torch.uint8).cpu().numpy())
+    assert np.isnan(qv[0]).all() and np.isnan(qv[2]).all()   # 0 * (1 / 0), and a NaN in the sum of squares
+
+
+def test_rows_beyond_32_bits():
+    """140,000 rows of 16,384 columns: offsets pass 2^31; the last rows are right."""
+    nb, dim = 140000, 16384
+    x = torch.zeros(nb, dim, dtype=torch.float16, device=DEV)
+    v = values(np.random.default_rng(10), (3, dim))
+    x[-3:] = torch.from_numpy(v).to(DEV).to(torch.float16)
+    q, s = q4a.quantize_fp8(x)
+    check_codes(q[-3:], s[-3:], host64(x[-3:]), "last rows")
+    assert int(q[:-3].view(torch.uint8).count_nonzero()) == 0
+    w = torch.ones(dim, dtype=torch.bfloat16, device=DEV)
+    q, s, _ = q4a.add_rmsnorm_fp8(x, w, q=q, scale=s)
+    n, _ = oracle.add_rmsnorm(x[-3:].cpu().numpy(), None, w.view(torch.int16).cpu().numpy().view(np.uint16))
+    check_codes(q[-3:], s[-3:], n, "last normalised rows", rel=NORM_TOL)
+
+
+# ---- 4-bit weights in 8 bits ------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("rows,in_dim", [(1, 64), (127, 128), (128, 192), (130, 576), (257, 64), (300, 2048),
+                                         (1280, 640)])
+def test_dequant(rows, in_dim):
+    rng = np.random.default_rng(rows + in_dim)
+    packed = rng.integers(0, 256, (rows, in_dim // 2)).astype(np.uint8)
+    sb = [wl.f32_to_bf16_bits(f) for f in (np.abs(rng.normal(0, 0.02, (rows, in_dim // 64))),
+                                           -8 * rng.normal(0, 0.01, (rows, in_dim // 64)))]
+    sb[0][0, 0] ^= 0x8000            # a negative scale
+    sb[0][-1, -1] = 0
+    d = [torch.from_numpy(a.view(np.int16)).to(DEV) for a in sb]
+    bw, w8 = guarded((rows, in_dim), F8, 2.0)
+    w8, ws = q4a.dequant_fp8(torch.from_numpy(packed).to(DEV), *d, out=w8)
+    w = oracle.dequant(packed, *sb, in_dim)
+    # W is one fused multiply-add: 2^-24 of itself
+    check_codes(w8, ws, w, f"dequant {rows}x{in_dim}", block_rows=128, rel=U)
+    check_guard(bw, rows, "rows behind the last")
+
+
+def test_dequant_special_values():
+    rng = np.random.default_rng(12)
+    packed = np.tile((np.arange(32) * 0x11 % 256).astype(np.uint8), (200, 4))    # [200][128]: 256 inputs
+    s = rng.normal(0, 1, (200, 4)).astype(np.float32)
+    b = rng.normal(0, 1, (200, 4)).astype(np.float32)
+    s[:128, 2:], b[:128, 2:] = 0.0, 0.0                                       # a block of zeros
+    b[140, 1] = np.nan
+    sb = [wl.f32_to_bf16_bits(a) for a in (s, b)]
+    w8, ws = q4a.dequant_fp8(torch.from_numpy(packed).to(DEV),
+                             *(torch.from_numpy(a.view(np.int16)).to(DEV) for a in sb))
+    v, sv = oracle.e4m3_values(w8.view(torch.uint8).cpu().numpy()), host64(ws)
+    assert (v[:128, 128:] == 0).all() and sv[0, 1] == np.float32(2.0 ** -100) / np.float32(448)
+    assert np.isnan(v[140, 64:128]).all() and np.isnan(v).sum() == 64 and np.isfinite(sv).all()
+
+
+# ---- products ---------------------------------------------------------------------------------------
+
+
+def fp8_operands(rng, nb, out_dim, in_dim):
+    """Codes and scales as the quantiser writes them, made on the host."""
+    x, w = values(rng, (nb, in_dim)), rng.normal(0, in_dim ** -0.5, (out_dim, in_dim))
+    w = w * np.exp(0.5 * rng.normal(0, 1, (out_dim, 1)))
+    out = []
+    for v, br in ((w, 128), (x, 1)):
+        s = oracle.e4m3_scales(v, br).astype(np.float32)
+        sv = np.repeat(np.repeat(s, br, 0)[: v.shape[0]], 128, 1)[:, : v.shape[1]]
+        out += [torch.from_numpy((v / sv).astype(np.float32)).to(F8), torch.from_numpy(s)]
+    return out
+
+
+def product_reference(ops):
+    w, ws, x, xs = ops
+    y, mag = oracle.gemm_e4m3(w.view(torch.uint8).numpy(), ws.numpy(), x.view(torch.uint8).numpy(), xs.numpy())
+    return y, (128 * 2.0 ** -23 + (xs.shape[1] + 2) * U) * mag
+
+
+def check_product(ops, t, what):
+    w, ws, x, xs = (a.to(DEV) for a in ops)
+    big, y = guarded((x.shape[0], w.shape[0]), TYPES[t], float("nan"))
+    q4a.gemm_fp8(w, ws, x, xs, out=y)
+    torch.cuda.synchronize()
+    q4a.check_device_error()
+    ref, err = product_reference(ops)
+    got = host64(y)
+    assert np.isfinite(got).all(), f"{what}: non-finite or unwritten"
+    bound = err + HALF_STEP[t] * (np.abs(ref) + err) + TINY[t]
+    worst = (np.abs(got - ref) / bound).max()
+    assert worst <= 1.0, f"{what}: off by {worst:.3g} of the bound"
+    check_guard(big, x.shape[0], f"{what}: rows behind the last")
+
+
+PRODUCTS = [(1, 1, 16), (1, 128, 128), (2, 130, 144), (7, 1000, 272), (8, 257, 4096), (13, 512, 12288), (16, 64, 640),
+            (17, 257, 656), (31, 4100, 256), (33, 96, 2064), (64, 384, 512), (65, 131, 1024), (100, 640, 400),
+            (128, 256, 512), (129, 384, 1040), (200, 1001, 1536), (257, 272, 272), (300, 520, 128), (513, 260, 640),
+            (1030, 300, 192)]
+
+
+@pytest.mark.parametrize("t", sorted(TYPES))
+@pytest.mark.parametrize("nb,out_dim,in_dim", PRODUCTS)
+def test_gemm(nb, out_dim, in_dim, t):
+    ops = fp8_operands(np.random.default_rng(nb + out_dim + in_dim), nb, out_dim, in_dim)
+    check_product(ops, t, f"gemm {nb} x {in_dim} -> {out_dim} {t}")
+
+
+@pytest.mark.parametrize("nb", [3, 40, 300])
+def test_gemm_any_scales(nb):
+    """Scales of any sign and size, zeros among them, as a checkpoint may hold them."""
+    rng = np.random.default_rng(nb)
+    w, ws, x, xs = fp8_operands(rng, nb, 300, 656)
+    ws = torch.from_numpy((rng.normal(0, 1, tuple(ws.shape)) * 2.0 ** rng.integers(-30, 30, tuple(ws.shape))).astype(np.float32))
+    xs = torch.from_numpy((rng.normal(0, 1, tuple(xs.shape)) * 2.0 ** rng.integers(-30, 30, tuple(xs.shape))).astype(np.float32))
+    ws[0, 1], xs[1, 2] = 0.0, 0.0
+    check_product([w, ws, x, xs], "f32", f"any scales {nb}")
+
+
+@pytest.mark.parametrize("nb", [2, 20, 150, 300])
+def test_gemm_nan_stays_in_its_rows(nb):
+    ops = fp8_operands(np.random.default_rng(50 + nb), nb, 300, 400)
+    w, ws, x, xs = (a.to(DEV) for a in ops)
+    clean = q4a.gemm_fp8(w, ws, x, xs)
+    x.view(torch.uint8)[1, 7] = 0x7F
+    w.view(torch.uint8)[130, 390] = 0xFF
+    y = host64(q4a.gemm_fp8(w, ws, x, xs))
+    assert np.isnan(y[1]).all() and np.isnan(y[:, 130]).all()
+    keep = np.ones(y.shape, bool)
+    keep[1], keep[:, 130] = False, False
+    assert np.array_equal(y[keep], host64(clean)[keep])
+
+
+def test_gemm_short_views():
+    """Bases that are 16-byte aligned and no more, and a y that is aligned to its element only."""
+    for nb, t in ((5, "f16"), (300, "f16"), (300, "f32"), (5, "f32")):
+        ops = fp8_operands(np.random.default_rng(60 + nb), nb, 260, 272)
+        w, ws, x, xs = ops
+        held = []
+        for a in (w, x):
+            buf = torch.zeros(a.numel() + 16, dtype=torch.uint8, device=DEV)
+            buf[16:] = a.view(torch.uint8).reshape(-1).to(DEV)
+            held.append(buf[16:].view(F8).view(a.shape))
+        y = torch.full((nb * 260 + 1,), float("nan"), dtype=TYPES[t], device=DEV)[1:].view(nb, 260)
+        sc = [torch.cat((torch.zeros(1), a.reshape(-1))).to(DEV)[1:].view(a.shape) for a in (ws, xs)]
+        q4a.gemm_fp8(held[0], sc[0], held[1], sc[1], out=y)
+        ref, err = product_reference(ops)
+        assert (np.abs(host64(y) - ref) <= err + HALF_STEP[t] * (np.abs(ref) + err)).all(), (nb, t)
+
+
+def gated_reference(ops):
+    y, err = product_reference(ops)
+    half = y.shape[1] // 2
+    g, u, eg, eu = y[:, :half], y[:, half:], err[:, :half], err[:, half:]
+    sg = g / (1 + np.exp(-g))
+    h = sg * u
+    return h, 1.1 * (np.abs(u) + eu) * eg + (np.abs(sg) + 1.1 * eg) * eu + 2.0 ** -20 * np.abs(h)
+
+
+@pytest.mark.parametrize("nb,inter,in_dim", [(1, 128, 64), (2, 128, 16), (3, 256, 528), (9, 640, 2048), (16, 384, 272),
+                                             (33, 128, 4096), (64, 256, 640), (100, 128, 256), (129, 640, 144),
+                                             (130, 384, 512), (257, 128, 640), (600, 256, 272)])
+def test_gate_up(nb, inter, in_dim):
+    ops = fp8_operands(np.random.default_rng(nb + inter + in_dim), nb, 2 * inter, in_dim)
+    w, ws, x, xs = (a.to(DEV) for a in ops)
+    bq, q = guarded((nb, inter), F8, 2.0)
+    bs, s = guarded((nb, inter // 128), torch.float32, 3.0)
+    q4a.gemm_fp8_gate_up_silu(w, ws, x, xs, q=q, scale=s)
+    torch.cuda.synchronize()
+    q4a.check_device_error()
+    h, err = gated_reference(ops)
+    check_codes(q, s, h, f"gate_up {nb} x {in_dim} -> {inter}", err=err)
+    check_guard(bq, nb, "codes behind the last row")
+    check_guard(bs, nb, "scales behind the last row")
+
+
+@pytest.mark.parametrize("nb", [2, 150, 300])
+def test_gate_up_zero_rows_and_nan(nb):
+    ops = fp8_operands(np.random.default_rng(70 + nb), nb, 512, 272)
+    ops[2].view(torch.uint8)[0] = 0
+    w, ws, x, xs = (a.to(DEV) for a in ops)
+    w.view(torch.uint8)[256 + 130, 3] = 0x7F         # an up row of the second block
+    q, s = q4a.gemm_fp8_gate_up_silu(w, ws, x, xs)
+    v, sv = oracle.e4m3_values(q.view(torch.uint8).cpu().numpy()), host64(s)
+    assert np.isnan(v[:, 130]).all() and np.isnan(v).sum() == nb and np.isfinite(sv).all()
+    assert (np.delete(v[0], 130) == 0).all() and (sv[0] == np.float32(2.0 ** -100) / np.float32(448)).all()
+
+
+def test_products_beyond_32_bits():
+    """140,000 rows of 16,384 columns into 24 outputs: the operand passes 2^31 bytes."""
+    nb, in_dim, out_dim = 140000, 16384, 24
+    w, ws, x3, xs3 = fp8_operands(np.random.default_rng(11), 3, out_dim, in_dim)
+    x = torch.zeros(nb, in_dim, dtype=F8, device=DEV)
+    xs = torch.ones(nb, in_dim // 128, device=DEV)
+    x.view(torch.uint8)[-3:] = x3.view(torch.uint8).to(DEV)
+    xs[-3:] = xs3.to(DEV)
+    y = q4a.gemm_fp8(w.to(DEV), ws.to(DEV), x, xs)
+    ref, err = product_reference([w, ws, x3, xs3])
+    assert (np.abs(host64(y[-3:]) - ref) <= err + U * np.abs(ref)).all()
+    assert int(y[:-3].count_nonzero()) == 0
+    # and as the weights
+    y = q4a.gemm_fp8(x, torch.ones(-(-nb // 128), in_dim // 128, device=DEV), w.to(DEV), torch.ones(24, 128, device=DEV))
+    one = [x3, torch.ones(1, 128), w, torch.ones(24, 128)]
+    ref, err = product_reference(one)
+    assert (np.abs(host64(y[:, -3:]) - ref) <= err + U * np.abs(ref)).all()
+    assert int(y[:, :-3].count_nonzero()) == 0
+
+
+# ---- together ---------------------------------------------------------------------------------------
+
+
+def layer(nb, hidden, inter, seed):
+    rng = np.random.default_rng(seed)
+    x, _ = typed(values(rng, (nb, hidden), 0.5), "f32")
+    res, _ = typed(values(rng, (nb, hidden), 2.0), "bf16")
+    nw = torch.from_numpy(wl.f32_to_bf16_bits(1 + 0.05 * rng.normal(0, 1, hidden)).view(np.int16)).to(DEV)
+    packed = []
+    for rows, cols in ((2 * inter, hidden), (hidden, inter)):
+        qm = [torch.from_numpy(rng.integers(0, 256, (rows, cols // 2)).astype(np.uint8)).to(DEV)]
+        s = np.abs(rng.normal(0, 0.5, (rows, cols // 64))) * cols ** -0.5
+        qm += [torch.from_numpy(wl.f32_to_bf16_bits(a).view(np.int16)).to(DEV) for a in (s, -7.5 * s)]
+        packed.append(q4a.dequant_fp8(*qm))
+    return x, res, nw, packed[0], packed[1]
+
+
+@pytest.mark.parametrize("nb,hidden,inter", [(1, 512, 256), (9, 640, 384), (150, 576, 256), (300, 512, 640)])
+def test_mlp_is_its_three_steps(nb, hidden, inter):
+    x, res, nw, gu, dn = layer(nb, hidden, inter, nb)
+    n, ns, x_new = q4a.add_rmsnorm_fp8(x, nw, residual=res)
+    h, hs = q4a.gemm_fp8_gate_up_silu(*gu, n, ns)
+    y = q4a.gemm_fp8(*dn, h, hs, out_dtype=torch.bfloat16)
+    hold = (torch.empty_like(n), torch.empty_like(ns)), (torch.empty_like(h), torch.empty_like(hs))
+    y2, x2 = q4a.mlp_fp8(x, nw, *gu, *dn, residual=res, out_dtype=torch.bfloat16, n=hold[0], h=hold[1])
+    for a, b in ((y, y2), (x_new, x2), (n, hold[0][0]), (ns, hold[0][1]), (h, hold[1][0]), (hs, hold[1][1])):
+        assert torch.equal(bits(a), bits(b))
+    # and the layer is near the same layer in 64 bits on the same 8-bit weights: three roundings to
+    # e4m3 (2^-4 of a value at most, each) on the way to sums that cancel
+    wv = [oracle.e4m3_values(q.view(torch.uint8).cpu().numpy())
+          * np.repeat(np.repeat(host64(s), 128, 0), 128, 1)[: q.shape[0], : q.shape[1]] for q, s in (gu, dn)]
+    xv = host64(x_new)
+    nv = xv / np.sqrt((xv ** 2).mean(1, keepdims=True) + 1e-6) * host64(nw.view(torch.bfloat16))
+    g = nv @ wv[0].T
+    hv = g[:, :inter] / (1 + np.exp(-g[:, :inter])) * g[:, inter:]
+    ref = hv @ wv[1].T
+    assert np.linalg.norm(host64(y) - ref) <= 0.1 * np.linalg.norm(ref)
+
+
+def test_mlp_captured_and_replayed():
+    """One graph of two layers' calls, replayed on new inputs, beside eager calls on another stream."""
+    nb, hidden, inter = 40, 512, 384
+    x, res, nw, gu, dn = layer(nb, hidden, inter, 21)
+    x_in, r_in = x.clone(), res.clone()
+    q4a.mlp_fp8(x_in, nw, *gu, *dn, residual=r_in)             # loaded before the capture
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y1, x1 = q4a.mlp_fp8(x_in, nw, *gu, *dn, residual=r_in)
+        y2, x2 = q4a.mlp_fp8(y1, nw, *gu, *dn, residual=x1)
+    for seed in (1, 2):
+        a, b = layer(nb, hidden, inter, 30 + seed)[:2]
+        x_in.copy_(a)
+        r_in.copy_(b)
+        g.replay()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        e1, n1 = q4a.mlp_fp8(a, nw, *gu, *dn, residual=b, stream=side)
+        e2, n2 = q4a.mlp_fp8(e1, nw, *gu, *dn, residual=n1, stream=side)
+        side.synchronize()
+        torch.cuda.synchronize()
+        for p, q in ((y1, e1), (x1, n1), (y2, e2), (x2, n2)):
+            assert torch.equal(bits(p), bits(q))
+
+
+def test_two_streams_at_once():
+    """The same calls on two streams at the same time give what they give alone."""
+    cases = [layer(nb, 640, 384, 40 + nb) for nb in (5, 200)]
+    alone = [q4a.mlp_fp8(x, nw, *gu, *dn, residual=res) for x, res, nw, gu, dn in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = []
+    for _ in range(20):
+        got.append([q4a.mlp_fp8(x, nw, *gu, *dn, residual=res, stream=st)
+                    for st, (x, res, nw, gu, dn) in zip(streams, cases)])
+    torch.cuda.synchronize()
+    for pair in got:
+        for (y, xn), (y0, x0) in zip(pair, alone):
+            assert torch.equal(bits(y), bits(y0)) and torch.equal(bits(xn), bits(x0))
+    q4a.check_device_error()
+
+
+@pytest.mark.parametrize("nb", [1, 16, 128, 500])
+def test_repeatable(nb):
+    w, ws, x, xs = (a.to(DEV) for a in fp8_operands(np.random.default_rng(80 + nb), nb, 1024, 4096))
+    first = q4a.gemm_fp8(w, ws, x, xs)
+    q, s = q4a.gemm_fp8_gate_up_silu(w, ws, x, xs)
+    for _ in range(10):
+        assert torch.equal(bits(q4a.gemm_fp8(w, ws, x, xs)), bits(first))
+        q2, s2 = q4a.gemm_fp8_gate_up_silu(w, ws, x, xs)
+        assert torch.equal(bits(q), bits(q2)) and torch.equal(bits(s), bits(s2))
+
+
+def test_dequantised_product_is_the_gemvs():
+    """dequant_fp8 then gemm_fp8 against gemv on the same 4-bit weights: apart by the roundings to
+    e4m3, 2^-4 of a weight and of an activation at most, on sums that cancel."""
+    rng = np.random.default_rng(90)
+    packed = torch.from_numpy(rng.integers(0, 256, (640, 1024)).astype(np.uint8)).to(DEV)
+    s = np.abs(rng.normal(0, 0.02, (640, 32)))
+    s, b = (torch.from_numpy(wl.f32_to_bf16_bits(a).view(np.int16)).to(DEV) for a in (s, -7.5 * s))
+    x = torch.from_numpy(rng.normal(0, 1, (48, 2048)).astype(np.float16)).to(DEV)
+    y = host64(q4a.gemm_fp8(*q4a.dequant_fp8(packed, s, b), *q4a.quantize_fp8(x)))
+    ref = host64(q4a.gemv(packed, s, b, x))
+    assert np.linalg.norm(y - ref) <= 0.1 * np.linalg.norm(ref)
