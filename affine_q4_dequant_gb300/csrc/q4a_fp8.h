@@ -49,6 +49,7 @@ struct Fp8Gemm {
     int64_t nb, out_dim, in_dim;
 };
 q4a_status launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t stream);
+q4a_status read_and_clear_gemm_fp8_error(uint32_t* word);   // after a stream synchronisation
 
 }  // namespace q4a
 

@@ -1,120 +1,490 @@
 // q4a_fp8_gemm.cu -- the block-scaled 8-bit product and its gated form:
 //     y[r][o] = sum_k xs[r][k] ws[o/128][k] sum_{i in block k} x[r][i] w[o][i]
-// A plain tiled kernel on the CUDA cores: 16 activation rows x 128 outputs a CTA.
+//     h[r][o] = silu(g) * u of a gate and an up row, in e4m3 with a scale per 128 columns
+//
+// The scales change every 128 columns, so the tensor cores sum one block of 128 columns at a time
+// (four tcgen05.mma of 32 columns into a fresh accumulator) and CUDA cores add the block's sum,
+// times its two scales, to fp32 registers: one fused multiply-add per output and block.
+//
+// The weights are the MMA's M (128 rows, one TMEM lane each) and the activation rows its N: one
+// weight row block has one scale, so an accumulator column's factor is xs[r][k] * ws[k], the same
+// for all lanes. A decode step's few rows then cost little beside the weights' bytes.
+//
+// CTA (352 threads), one tile of T x 128 weight rows (T = 2 in the gated form: the gate rows and
+// the up rows with the same index) x N activation rows x a share of the column blocks:
+//   warp 0      TMA producer: the block's weights [T][128 rows][128 bytes] and activations
+//               [N rows][128 bytes] into a ring of S stages
+//   warp 1      allocates TMEM; issues the MMAs into a ring of AB accumulators
+//   warps 2..9  add the blocks: thread = one weight row and CPT of the columns
+//   warp 10     the blocks' factors xs * ws, AB blocks ahead
+// Few tiles (short matrices, few rows) split the column blocks over a cluster of C CTAs; their
+// sums meet in distributed shared memory, in rank order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
-#include "q4a_device.cuh"
+#include <string.h>
+
+#include <map>
+#include <mutex>
+
 #include "q4a_fp8.h"
 #include "q4a_internal.h"
+#include "q4a_tcgen05.cuh"
 
 namespace q4a {
 namespace {
 
-constexpr int kSimpleRows = 16;   // activation rows of a CTA
-constexpr int kSimpleK = 32;      // columns staged at a time
+constexpr int kNwWarps = 11;
+constexpr int kNwThreads = kNwWarps * 32;
+constexpr int kNwAdd0 = 2;             // first adding warp
+constexpr int kNwAddWarps = 8;
+constexpr int kNwScaleWarp = kNwAdd0 + kNwAddWarps;
+constexpr int kNwTile = 128 * 128;     // bytes of 128 rows of one block
+constexpr int kNwMaxCluster = 8;
 
-__device__ __forceinline__ float e4m3_f32(uint8_t v) {
-    __nv_fp8_e4m3 f;
-    f.__x = v;
-    return (float)f;
+constexpr int pow2_at_least(int v) {
+    int p = 32;
+    while (p < v) p *= 2;
+    return p;
 }
 
-// acc[j] = (W x) of activation row row0 + (tid >> 7) * 8 + j and weight row w_row0 + (tid & 127),
-// for weight rows below w_rows.
-__device__ void product_tile(const Fp8Gemm& p, int64_t row0, int64_t w_row0, int64_t w_rows, float (&acc)[8]) {
-    __shared__ float s_w[kFp8Block][kSimpleK + 1];
-    __shared__ float s_x[kSimpleRows][kSimpleK + 1];
-    const int64_t nblk = (p.in_dim + kFp8Block - 1) / kFp8Block;
-    const int col = threadIdx.x & 127, half = threadIdx.x >> 7;
-    for (int j = 0; j < 8; ++j) acc[j] = 0.f;
-    for (int64_t kb = 0; kb < nblk; ++kb) {
-        float part[8] = {};
-        for (int64_t k0 = kb * kFp8Block; k0 < (kb + 1) * kFp8Block && k0 < p.in_dim; k0 += kSimpleK) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < kFp8Block * kSimpleK; i += 256) {
-                const int64_t r = w_row0 + i / kSimpleK, k = k0 + i % kSimpleK;
-                s_w[i / kSimpleK][i % kSimpleK] = r < w_rows && k < p.in_dim ? e4m3_f32(p.w[r * p.in_dim + k]) : 0.f;
+// Geometry of one kernel: N activation rows, T weight tiles, R CTAs per SM.
+template <int N, int T>
+struct Narrow {
+    static constexpr int CPT = T == 2 ? N : N / 2;          // accumulator columns of an adding thread
+    static constexpr int R = CPT <= 32 ? 2 : 1;             // registers: 2 x 352 threads leave 92 a thread
+    static constexpr int stage = T * kNwTile + N * 128;
+    static constexpr int budget = R == 2 ? 106 * 1024 : 216 * 1024;
+    static constexpr int fit = budget / stage;
+    static constexpr int S = fit > 8 ? 8 : fit;
+    static constexpr int acc_fit = 512 / R / (T * N);
+    static constexpr int AB = acc_fit > 8 ? 8 : acc_fit;
+    static constexpr int tmem_cols = pow2_at_least(AB * T * N);
+    static constexpr int ring = 0;
+    static constexpr int scales = ring + S * stage;          // fp32 [AB][T][N]
+    static constexpr int bars = scales + AB * T * N * 4;     // full[S] empty[S] acc_full[AB] acc_empty[AB] scale_full[AB]
+    static constexpr int slot = bars + (2 * S + 3 * AB) * 8;
+    static constexpr int abort = slot + 4;
+    static constexpr int total = abort + 4;
+    static constexpr int smem = total + 1024;
+    static_assert(S >= 2 && AB >= 2, "double buffering");
+    static_assert(T * N * 512 <= S * stage, "the partial sums reuse the ring");
+    static_assert(AB * T * N <= 512 / R, "TMEM of R CTAs");
+    static_assert(smem <= (R == 2 ? 113 : 227) * 1024, "shared memory of R CTAs");
+};
+
+struct NarrowParams {
+    CUtensorMap tmap_w;    // e4m3 [weight rows][in_dim], box 128 bytes x 128 rows, 128-byte swizzle
+    CUtensorMap tmap_x;    // e4m3 [nb][in_dim], box 128 bytes x N rows, 128-byte swizzle
+    Fp8Gemm g;
+    int32_t nk;            // column blocks
+    int32_t n_tiles;       // tiles of N activation rows
+    int32_t cluster;
+    int32_t y_vec;         // rows of y allow 4-element stores
+};
+
+__device__ __forceinline__ uint32_t nw_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void nw_cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %4, %5;\n"
+        " ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [a];\n}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(addr), "r"(rank)
+        : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float4 lds_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
+}
+
+// acc (two fp32) += d * s, element by element.
+__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t d0, uint32_t d1, uint64_t s) {
+    asm("{\n .reg .b64 d;\n mov.b64 d, {%1, %2};\n fma.rn.f32x2 %0, d, %3, %0;\n}" : "+l"(acc) : "r"(d0), "r"(d1), "l"(s));
+}
+__device__ __forceinline__ void lds_u64x2(uint32_t addr, uint64_t& a, uint64_t& b) {
+    asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr));
+}
+
+// acc[0..CPT) += (accumulator columns) * (their factors in shared memory). The next columns' TMEM
+// load is in flight while the current ones are added.
+template <int CPT>
+__device__ __forceinline__ void add_block(uint64_t (&acc)[CPT / 2], uint32_t taddr, uint32_t saddr) {
+    if constexpr (CPT == 8) {
+        uint32_t d[8];
+        tc_ld8_issue(taddr, d);
+        uint64_t s[4];
+        lds_u64x2(saddr, s[0], s[1]);
+        lds_u64x2(saddr + 16, s[2], s[3]);
+        tc_ld8_wait(d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fma2(acc[i], d[2 * i], d[2 * i + 1], s[i]);
+    } else {
+        uint32_t d[2][16];
+        tc_ld16_issue(taddr, d[0]);
+        tc_ld16_wait(d[0]);
+#pragma unroll
+        for (int c = 0; c < CPT / 16; ++c) {
+            if (c + 1 < CPT / 16) tc_ld16_issue(taddr + 16 * (c + 1), d[(c + 1) & 1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint64_t s0, s1;
+                lds_u64x2(saddr + (uint32_t)(16 * c + 4 * i) * 4u, s0, s1);
+                fma2(acc[8 * c + 2 * i], d[c & 1][4 * i], d[c & 1][4 * i + 1], s0);
+                fma2(acc[8 * c + 2 * i + 1], d[c & 1][4 * i + 2], d[c & 1][4 * i + 3], s1);
             }
-            for (int i = threadIdx.x; i < kSimpleRows * kSimpleK; i += 256) {
-                const int64_t r = row0 + i / kSimpleK, k = k0 + i % kSimpleK;
-                s_x[i / kSimpleK][i % kSimpleK] = r < p.nb && k < p.in_dim ? e4m3_f32(p.x[r * p.in_dim + k]) : 0.f;
-            }
-            __syncthreads();
-            for (int k = 0; k < kSimpleK; ++k)
-                for (int j = 0; j < 8; ++j) part[j] = fmaf(s_w[col][k], s_x[half * 8 + j][k], part[j]);
-        }
-        const float ws = w_row0 < w_rows ? p.w_scale[w_row0 / kFp8Block * nblk + kb] : 0.f;
-        for (int j = 0; j < 8; ++j) {
-            const int64_t r = row0 + half * 8 + j;
-            if (r < p.nb) acc[j] = fmaf(part[j], p.x_scale[r * nblk + kb] * ws, acc[j]);
+            if (c + 1 < CPT / 16) tc_ld16_wait(d[(c + 1) & 1]);
         }
     }
 }
 
-__global__ void __launch_bounds__(256) gemm_fp8_kernel(const Fp8Gemm p) {
-    grid_dep_wait();
-    grid_dep_launch();
-    const int64_t nt = (p.nb + kSimpleRows - 1) / kSimpleRows;
-    const int64_t row0 = blockIdx.x % nt * kSimpleRows, o0 = blockIdx.x / nt * kFp8Block;
-    const int col = threadIdx.x & 127, half = threadIdx.x >> 7;
-    float acc[8];
-    product_tile(p, row0, o0, p.out_dim, acc);
-    for (int j = 0; j < 8; ++j) {
-        const int64_t r = row0 + half * 8 + j, at = r * p.out_dim + o0 + col;
-        if (r >= p.nb || o0 + col >= p.out_dim) continue;
-        if (p.y_type == Q4A_F32) static_cast<float*>(p.y)[at] = acc[j];
-        else if (p.y_type == Q4A_F16) static_cast<__half*>(p.y)[at] = __float2half_rn(acc[j]);
-        else static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(acc[j]);
-    }
-}
+__device__ __forceinline__ float gated(float g, float u) { return g / (1.f + expf(-g)) * u; }
 
-__global__ void __launch_bounds__(256) gate_up_fp8_kernel(const Fp8Gemm p) {
-    __shared__ float s_max[8][8];
-    grid_dep_wait();
+template <int N, int T>
+__global__ void __launch_bounds__(kNwThreads, Narrow<N, T>::R) narrow_kernel(const __grid_constant__ NarrowParams p) {
+    using G = Narrow<N, T>;
+    constexpr int S = G::S, AB = G::AB, CPT = G::CPT;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::bars);
+    uint64_t* empty = full + S;
+    uint64_t* acc_full = empty + S;
+    uint64_t* acc_empty = acc_full + AB;
+    uint64_t* scale_full = acc_empty + AB;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + G::slot);
+    volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + G::abort);
+    float* scales = reinterpret_cast<float*>(smem + G::scales);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int C = p.cluster;
+    const int rank = C > 1 ? (int)nw_rank() : 0;
+    const int tile = (int)(blockIdx.x / (unsigned)C);
+    const int64_t n0 = (int64_t)(tile % p.n_tiles) * N;          // first activation row
+    const int64_t o0 = (int64_t)(tile / p.n_tiles) * 128;        // first weight row (of the gate)
+    const int kb0 = (int)((int64_t)rank * p.nk / C), kb1 = (int)((int64_t)(rank + 1) * p.nk / C);
+
     grid_dep_launch();
-    const int64_t nt = (p.nb + kSimpleRows - 1) / kSimpleRows;
-    const int64_t row0 = blockIdx.x % nt * kSimpleRows, o0 = blockIdx.x / nt * kFp8Block;
-    const int col = threadIdx.x & 127, half = threadIdx.x >> 7;
-    float g[8], u[8];
-    product_tile(p, row0, o0, 2 * p.out_dim, g);
-    product_tile(p, row0, p.out_dim + o0, 2 * p.out_dim, u);
-    for (int j = 0; j < 8; ++j) {
-        g[j] = g[j] / (1.f + expf(-g[j])) * u[j];
-        float m = fabsf(g[j]);
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5][j] = m;
+    if (threadIdx.x == 0) {
+        prefetch_tensormap(&p.tmap_w);
+        prefetch_tensormap(&p.tmap_x);
+        for (int i = 0; i < S; ++i) {
+            mbar_init(smem_addr(full + i), 1);
+            mbar_init(smem_addr(empty + i), 1);
+        }
+        for (int i = 0; i < AB; ++i) {
+            mbar_init(smem_addr(acc_full + i), 1);
+            mbar_init(smem_addr(acc_empty + i), kNwAddWarps);
+            mbar_init(smem_addr(scale_full + i), 1);
+        }
+        *abort_flag = 0u;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (warp == 1) tc_alloc(smem_addr(tmem_slot), G::tmem_cols);
+    tc_fence_before();
     __syncthreads();
-    for (int j = 0; j < 8; ++j) {
-        const int64_t r = row0 + half * 8 + j;
-        float m = 0.f;
-        for (int i = 0; i < 4; ++i) m = fmaxf(m, s_max[half * 4 + i][j]);
-        const float scale = fp8_scale(m), inv = 1.f / scale;
-        if (r >= p.nb) continue;
-        p.q[r * p.out_dim + o0 + col] = (uint8_t)e4m3x2(g[j] * inv, 0.f);
-        if (col == 0) p.scale[r * (p.out_dim / kFp8Block) + o0 / kFp8Block] = scale;
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    grid_dep_wait();   // operands, scales and outputs may belong to the previous kernel of the stream
+
+    if (warp == 0) {
+        if (lane == 0) {
+            for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
+                const int s = i % S;
+                if (i >= S) mbar_wait(smem_addr(empty + s), (uint32_t)(i / S - 1) & 1u, abort_flag);
+                const uint32_t bar = smem_addr(full + s), at = smem_addr(smem + G::ring + s * G::stage);
+                mbar_arrive_expect_tx(bar, G::stage);
+                tma_load_2d(at, &p.tmap_w, kb * kFp8Block, (int)o0, bar);
+                if (T == 2) tma_load_2d(at + kNwTile, &p.tmap_w, kb * kFp8Block, (int)(p.g.out_dim + o0), bar);
+                tma_load_2d(at + T * kNwTile, &p.tmap_x, kb * kFp8Block, (int)n0, bar);
+            }
+            // after a give-up nobody has waited for the last copies: none may land after the CTA is gone
+            if (*abort_flag)
+                for (int i = kb1 - kb0 < S ? 0 : kb1 - kb0 - S; i < kb1 - kb0; ++i)
+                    mbar_drain(smem_addr(full + i % S), (uint32_t)(i / S) & 1u);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        constexpr uint32_t idesc = idesc_f8(128, N);
+        for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
+            const int s = i % S, buf = i % AB;
+            if (i >= AB) mbar_wait(smem_addr(acc_empty + buf), (uint32_t)(i / AB - 1) & 1u, abort_flag);
+            mbar_wait(smem_addr(full + s), (uint32_t)(i / S) & 1u, abort_flag);
+            __syncwarp();
+            tc_fence_after();
+            const uint32_t at = smem_addr(smem + G::ring + s * G::stage);
+            if (elect_one()) {
+                const uint64_t xd = smem_desc(at + T * kNwTile);
+#pragma unroll
+                for (int t = 0; t < T; ++t) {
+                    const uint64_t wd = smem_desc(at + t * kNwTile);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tc_mma_f8(tmem + (uint32_t)((buf * T + t) * N), wd + 2u * k, xd + 2u * k, idesc, (uint32_t)k);
+                }
+                tc_commit(smem_addr(empty + s));
+                tc_commit(smem_addr(acc_full + buf));
+            }
+            __syncwarp();
+        }
+        if (*abort_flag) mbar_drain(smem_addr(acc_full + (kb1 - kb0 - 1) % AB), (uint32_t)((kb1 - kb0 - 1) / AB) & 1u);
+    } else if (warp == kNwScaleWarp) {
+        // four blocks' scales at a time, the next four loaded while these wait for their slots
+        constexpr int NL = (N + 31) / 32;
+        const int64_t left = p.g.nb - n0;
+        float v[NL][4], w[T][4], vn[NL][4], wn[T][4];
+        auto load = [&](int kb, float (&a)[NL][4], float (&b)[T][4]) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                for (int l = 0; l < NL; ++l) {
+                    const int n = l * 32 + lane;
+                    a[l][j] = kb + j < kb1 && n < N && n < left ? __ldg(p.g.x_scale + (n0 + n) * p.nk + kb + j) : 0.f;
+                }
+#pragma unroll
+                for (int t = 0; t < T; ++t)
+                    b[t][j] = kb + j < kb1
+                                  ? __ldg(p.g.w_scale + (t * p.g.out_dim + o0) / kFp8Block * p.nk + kb + j) : 0.f;
+            }
+        };
+        load(kb0, v, w);
+        for (int kb = kb0, i = 0; kb < kb1; kb += 4) {
+            load(kb + 4, vn, wn);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (kb + j < kb1) {
+                    const int buf = i % AB;
+                    if (i >= AB) mbar_wait(smem_addr(acc_empty + buf), (uint32_t)(i / AB - 1) & 1u, abort_flag);
+#pragma unroll
+                    for (int t = 0; t < T; ++t)
+#pragma unroll
+                        for (int l = 0; l < NL; ++l)
+                            if (l * 32 + lane < N) scales[(buf * T + t) * N + l * 32 + lane] = v[l][j] * w[t][j];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(scale_full + buf));
+                    ++i;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                for (int l = 0; l < NL; ++l) v[l][j] = vn[l][j];
+#pragma unroll
+                for (int t = 0; t < T; ++t) w[t][j] = wn[t][j];
+            }
+        }
+    } else {
+        const int wg = (warp - kNwAdd0) >> 2, quarter = warp & 3;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(wg * CPT);
+        const uint32_t sbase = smem_addr(scales) + (uint32_t)(wg * CPT) * 4u;
+        uint64_t acc[CPT / 2];
+#pragma unroll
+        for (int c = 0; c < CPT / 2; ++c) acc[c] = 0;
+        for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
+            const int buf = i % AB;
+            mbar_wait(smem_addr(scale_full + buf), (uint32_t)(i / AB) & 1u, abort_flag);
+            mbar_wait(smem_addr(acc_full + buf), (uint32_t)(i / AB) & 1u, abort_flag);
+            tc_fence_after();
+            add_block<CPT>(acc, lanes + (uint32_t)(buf * T * N), sbase + (uint32_t)(buf * T * N) * 4u);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(acc_empty + buf));
+        }
+        // every stage has been multiplied: the ring holds the partial sums [T][N][128 rows]
+        const uint32_t part = smem_addr(smem + G::ring) + (uint32_t)((wg * CPT) * 128 + quarter * 32 + lane) * 4u;
+#pragma unroll
+        for (int c = 0; c < CPT / 2; ++c) {
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(part + (uint32_t)(2 * c) * 512u), "r"((uint32_t)acc[c]) : "memory");
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(part + (uint32_t)(2 * c + 1) * 512u), "r"((uint32_t)(acc[c] >> 32))
+                         : "memory");
+        }
     }
+
+    tc_fence_before();
+    __syncwarp();
+    if (C > 1) nw_cluster_sync();
+    else __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tc_dealloc(tmem, G::tmem_cols);
+
+    // A warp takes an activation row, a lane 4 of its 128 outputs; the ranks share the rows.
+    const uint32_t ring = smem_addr(smem + G::ring) + (uint32_t)lane * 16u;
+    const int rows = (int)(p.g.nb - n0 < N ? p.g.nb - n0 : N);
+    auto total = [&](int tn) {
+        if (C == 1) return lds_f4(ring + (uint32_t)tn * 512u);
+        float4 v[kNwMaxCluster];
+#pragma unroll
+        for (int q = 0; q < kNwMaxCluster; ++q)
+            if (q < C) v[q] = ld_cluster_f4(ring + (uint32_t)tn * 512u, (uint32_t)q);
+        float4 a = v[0];
+#pragma unroll
+        for (int q = 1; q < kNwMaxCluster; ++q)
+            if (q < C) a.x += v[q].x, a.y += v[q].y, a.z += v[q].z, a.w += v[q].w;
+        return a;
+    };
+    if (warp < 8) {
+        for (int n = rank * 8 + warp; n < rows; n += 8 * C) {
+            const int64_t o = o0 + 4 * lane, row = n0 + n;
+            float4 a = total(n);
+            if (T == 2) {
+                const float4 u = total(N + n);
+                a = make_float4(gated(a.x, u.x), gated(a.y, u.y), gated(a.z, u.z), gated(a.w, u.w));
+                float amax = fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w)));
+#pragma unroll
+                for (int s = 16; s > 0; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
+                const float scale = fp8_scale(amax), inv = 1.f / scale;
+                *reinterpret_cast<uint32_t*>(p.g.q + row * p.g.out_dim + o) =
+                    e4m3x4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+                if (lane == 0) p.g.scale[row * (p.g.out_dim / kFp8Block) + o0 / kFp8Block] = scale;
+            } else {
+                const int64_t at = row * p.g.out_dim + o;
+                const float f[4] = {a.x, a.y, a.z, a.w};
+                if (p.g.y_type == Q4A_F32) {
+                    float* y = static_cast<float*>(p.g.y) + at;
+                    if (p.y_vec && o < p.g.out_dim) *reinterpret_cast<float4*>(y) = a;
+                    else
+                        for (int j = 0; j < 4; ++j)
+                            if (o + j < p.g.out_dim) y[j] = f[j];
+                } else {
+                    uint16_t* y = static_cast<uint16_t*>(p.g.y) + at;
+                    uint16_t h[4];
+                    for (int j = 0; j < 4; ++j)
+                        h[j] = p.g.y_type == Q4A_F16 ? __half_as_ushort(__float2half_rn(f[j]))
+                                                     : __bfloat16_as_ushort(__float2bfloat16_rn(f[j]));
+                    if (p.y_vec && o < p.g.out_dim)
+                        *reinterpret_cast<uint2*>(y) = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+                    else
+                        for (int j = 0; j < 4; ++j)
+                            if (o + j < p.g.out_dim) y[j] = h[j];
+                }
+            }
+        }
+    }
+    __syncwarp();
+    if (C > 1) nw_cluster_sync();   // no CTA exits while the others read its sums
+}
+
+// ---- host side ---------------------------------------------------------------------------
+
+// e4m3 rows [rows][in_dim] in boxes of 128 bytes x box_rows.
+CUresult rows_map(CUtensorMap* m, const uint8_t* base, int64_t rows, int64_t in_dim, int box_rows) {
+    const cuuint64_t dims[2] = {(cuuint64_t)in_dim, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)in_dim};
+    const cuuint32_t box[2] = {(cuuint32_t)kFp8Block, (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1u, 1u};
+    return encode_tiled_cached(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box, estr,
+                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+q4a_status sm_count(int* dev, int* sms) {
+    static std::mutex mu;
+    static std::map<int, int> cache;
+    cudaError_t e = cudaGetDevice(dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    std::lock_guard<std::mutex> lock(mu);
+    int& n = cache[*dev];
+    if (n <= 0) {
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, *dev);
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    *sms = n;
+    return Q4A_OK;
+}
+
+// cudaFuncSetAttribute once per kernel and device.
+template <typename K>
+q4a_status allow_smem(K kernel, int dev, int bytes) {
+    static std::mutex mu;
+    static std::map<std::pair<const void*, int>, bool> done;
+    std::lock_guard<std::mutex> lock(mu);
+    bool& d = done[{reinterpret_cast<const void*>(kernel), dev}];
+    if (!d) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return cuda_fail(e);
+        d = true;
+    }
+    return Q4A_OK;
+}
+
+template <int N, int T>
+q4a_status launch_narrow(const Fp8Gemm& g, int dev, int sms, cudaStream_t stream) {
+    using G = Narrow<N, T>;
+    NarrowParams p;
+    memset(&p, 0, sizeof(p));
+    CUresult r = rows_map(&p.tmap_w, g.w, T * g.out_dim, g.in_dim, 128);
+    if (r != CUDA_SUCCESS) return cuda_fail_drv(r);
+    r = rows_map(&p.tmap_x, g.x, g.nb, g.in_dim, N);
+    if (r != CUDA_SUCCESS) return cuda_fail_drv(r);
+    p.g = g;
+    p.nk = (int32_t)((g.in_dim + kFp8Block - 1) / kFp8Block);
+    p.n_tiles = (int32_t)((g.nb + N - 1) / N);
+    const int64_t size = fp8_type_bytes(g.y_type);
+    p.y_vec = g.out_dim % 4 == 0 && reinterpret_cast<uintptr_t>(g.y) % (4 * size) == 0;
+    const int64_t tiles = (g.out_dim + 127) / 128 * p.n_tiles;
+    int64_t C = (int64_t)sms * G::R / tiles;   // as many CTAs as run at once
+    C = C > kNwMaxCluster ? kNwMaxCluster : C;
+    C = C > p.nk ? p.nk : C;
+    C = C < 1 ? 1 : C;
+    p.cluster = (int32_t)C;
+    if (tiles * C > ((int64_t)1 << 31) - 1) return Q4A_ERR_UNSUPPORTED;
+    const q4a_status st = allow_smem(narrow_kernel<N, T>, dev, G::smem);
+    if (st != Q4A_OK) return st;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)C;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(tiles * C), 1, 1);
+    cfg.blockDim = dim3(kNwThreads, 1, 1);
+    cfg.dynamicSmemBytes = G::smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = C > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, narrow_kernel<N, T>, p);
+    return e == cudaSuccess ? Q4A_OK : cuda_fail(e);
 }
 
 }  // namespace
 
 q4a_status launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t stream) {
-    const int64_t tiles = (g.nb + kSimpleRows - 1) / kSimpleRows * ((g.out_dim + kFp8Block - 1) / kFp8Block);
-    if (tiles > ((int64_t)1 << 31) - 1) return Q4A_ERR_UNSUPPORTED;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)tiles, 1, 1);
-    cfg.blockDim = dim3(256, 1, 1);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = g.q ? cudaLaunchKernelEx(&cfg, gate_up_fp8_kernel, g)
-                              : cudaLaunchKernelEx(&cfg, gemm_fp8_kernel, g);
-    return e == cudaSuccess ? Q4A_OK : cuda_fail(e);
+    int dev = 0, sms = 0;
+    const q4a_status st = sm_count(&dev, &sms);
+    if (st != Q4A_OK) return st;
+    if (g.q) {
+        if (g.nb <= 16) return launch_narrow<16, 2>(g, dev, sms, stream);
+        if (g.nb <= 32) return launch_narrow<32, 2>(g, dev, sms, stream);
+        if (g.nb <= 64) return launch_narrow<64, 2>(g, dev, sms, stream);
+        return launch_narrow<128, 2>(g, dev, sms, stream);
+    }
+    if (g.nb <= 16) return launch_narrow<16, 1>(g, dev, sms, stream);
+    if (g.nb <= 32) return launch_narrow<32, 1>(g, dev, sms, stream);
+    if (g.nb <= 64) return launch_narrow<64, 1>(g, dev, sms, stream);
+    if (g.nb <= 128) return launch_narrow<128, 1>(g, dev, sms, stream);
+    return launch_narrow<256, 1>(g, dev, sms, stream);
+}
+
+q4a_status read_and_clear_gemm_fp8_error(uint32_t* word) {
+    uint32_t v = 0, zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_device_error, sizeof(v));
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (v) {
+        e = cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero));
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    *word = v;
+    return Q4A_OK;
 }
 
 }  // namespace q4a
