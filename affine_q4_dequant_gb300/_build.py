@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libq4a.so")
 BUILD_DIR = os.path.join(ROOT, "_build", "q4a")
 SOURCES = ["q4a_api.cu", "q4a_gemv.cu", "q4a_dense_tc.cu", "q4a_elementwise.cu", "q4a_fp8_rows.cu",
-           "q4a_fp8_gemm.cu"]
+           "q4a_fp8_gemm.cu", "q4a_fp8_wide.cu"]
 HEADERS = [os.path.join(CSRC, "q4a_internal.h"), os.path.join(CSRC, "q4a_device.cuh"),
            os.path.join(CSRC, "q4a_prefill.h"), os.path.join(CSRC, "q4a_fp8.h"), os.path.join(CSRC, "q4a_tcgen05.cuh"),
            os.path.join(ROOT, "include", "q4a.h")]

@@ -720,7 +720,10 @@ q4a_status q4a_check_device_error(q4a_stream_t stream) {
     uint32_t word_f8 = 0;
     st = read_and_clear_gemm_fp8_error(&word_f8);
     if (st != Q4A_OK) return st;
-    return (word | word_tc | word_f8) ? Q4A_ERR_TIMEOUT : Q4A_OK;
+    uint32_t word_wide = 0;
+    st = read_and_clear_fp8_wide_error(&word_wide);
+    if (st != Q4A_OK) return st;
+    return (word | word_tc | word_f8 | word_wide) ? Q4A_ERR_TIMEOUT : Q4A_OK;
 }
 
 }  // extern "C"

@@ -1,6 +1,7 @@
 // q4a_fp8.h -- the 8-bit (e4m3, block-scaled) operators' launchers, called by the C ABI.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -51,9 +52,24 @@ struct Fp8Gemm {
 q4a_status launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t stream);
 q4a_status read_and_clear_gemm_fp8_error(uint32_t* word);   // after a stream synchronisation
 
+// The form for many activation rows (q4a_fp8_wide.cu).
+q4a_status launch_gemm_fp8_wide(const Fp8Gemm& g, cudaStream_t stream);
+q4a_status read_and_clear_fp8_wide_error(uint32_t* word);
+
+// e4m3 rows [rows][in_dim] in boxes of 128 bytes x box_rows, 128-byte swizzle.
+CUresult fp8_rows_map(CUtensorMap* m, const uint8_t* base, int64_t rows, int64_t in_dim, int box_rows);
+// The current device and its SM count.
+q4a_status fp8_sm_count(int* dev, int* sms);
+
 }  // namespace q4a
 
 #ifdef __CUDACC__
+#include <map>
+#include <mutex>
+#include <utility>
+
+#include "q4a_internal.h"
+
 namespace q4a {
 namespace {
 
@@ -69,6 +85,23 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 
 // A block's scale from its largest magnitude (fmaxf drops a NaN, so the scale is the other values').
 __device__ __forceinline__ float fp8_scale(float amax) { return fmaxf(amax, kFp8Floor) / kFp8Top; }
+
+__device__ __forceinline__ float gated(float g, float u) { return g / (1.f + expf(-g)) * u; }
+
+// cudaFuncSetAttribute once per kernel and device.
+template <typename K>
+q4a_status fp8_allow_smem(K kernel, int dev, int bytes) {
+    static std::mutex mu;
+    static std::map<std::pair<const void*, int>, bool> done;
+    std::lock_guard<std::mutex> lock(mu);
+    bool& d = done[{reinterpret_cast<const void*>(kernel), dev}];
+    if (!d) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return cuda_fail(e);
+        d = true;
+    }
+    return Q4A_OK;
+}
 
 }  // namespace
 }  // namespace q4a

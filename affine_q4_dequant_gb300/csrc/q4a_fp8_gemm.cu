@@ -148,8 +148,6 @@ __device__ __forceinline__ void add_block(uint64_t (&acc)[CPT / 2], uint32_t tad
     }
 }
 
-__device__ __forceinline__ float gated(float g, float u) { return g / (1.f + expf(-g)) * u; }
-
 template <int N, int T>
 __global__ void __launch_bounds__(kNwThreads, Narrow<N, T>::R) narrow_kernel(const __grid_constant__ NarrowParams p) {
     using G = Narrow<N, T>;
@@ -375,55 +373,14 @@ __global__ void __launch_bounds__(kNwThreads, Narrow<N, T>::R) narrow_kernel(con
 
 // ---- host side ---------------------------------------------------------------------------
 
-// e4m3 rows [rows][in_dim] in boxes of 128 bytes x box_rows.
-CUresult rows_map(CUtensorMap* m, const uint8_t* base, int64_t rows, int64_t in_dim, int box_rows) {
-    const cuuint64_t dims[2] = {(cuuint64_t)in_dim, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)in_dim};
-    const cuuint32_t box[2] = {(cuuint32_t)kFp8Block, (cuuint32_t)box_rows};
-    const cuuint32_t estr[2] = {1u, 1u};
-    return encode_tiled_cached(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box, estr,
-                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-}
-
-q4a_status sm_count(int* dev, int* sms) {
-    static std::mutex mu;
-    static std::map<int, int> cache;
-    cudaError_t e = cudaGetDevice(dev);
-    if (e != cudaSuccess) return cuda_fail(e);
-    std::lock_guard<std::mutex> lock(mu);
-    int& n = cache[*dev];
-    if (n <= 0) {
-        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, *dev);
-        if (e != cudaSuccess) return cuda_fail(e);
-    }
-    *sms = n;
-    return Q4A_OK;
-}
-
-// cudaFuncSetAttribute once per kernel and device.
-template <typename K>
-q4a_status allow_smem(K kernel, int dev, int bytes) {
-    static std::mutex mu;
-    static std::map<std::pair<const void*, int>, bool> done;
-    std::lock_guard<std::mutex> lock(mu);
-    bool& d = done[{reinterpret_cast<const void*>(kernel), dev}];
-    if (!d) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != cudaSuccess) return cuda_fail(e);
-        d = true;
-    }
-    return Q4A_OK;
-}
-
 template <int N, int T>
 q4a_status launch_narrow(const Fp8Gemm& g, int dev, int sms, cudaStream_t stream) {
     using G = Narrow<N, T>;
     NarrowParams p;
     memset(&p, 0, sizeof(p));
-    CUresult r = rows_map(&p.tmap_w, g.w, T * g.out_dim, g.in_dim, 128);
+    CUresult r = fp8_rows_map(&p.tmap_w, g.w, T * g.out_dim, g.in_dim, 128);
     if (r != CUDA_SUCCESS) return cuda_fail_drv(r);
-    r = rows_map(&p.tmap_x, g.x, g.nb, g.in_dim, N);
+    r = fp8_rows_map(&p.tmap_x, g.x, g.nb, g.in_dim, N);
     if (r != CUDA_SUCCESS) return cuda_fail_drv(r);
     p.g = g;
     p.nk = (int32_t)((g.in_dim + kFp8Block - 1) / kFp8Block);
@@ -437,7 +394,7 @@ q4a_status launch_narrow(const Fp8Gemm& g, int dev, int sms, cudaStream_t stream
     C = C < 1 ? 1 : C;
     p.cluster = (int32_t)C;
     if (tiles * C > ((int64_t)1 << 31) - 1) return Q4A_ERR_UNSUPPORTED;
-    const q4a_status st = allow_smem(narrow_kernel<N, T>, dev, G::smem);
+    const q4a_status st = fp8_allow_smem(narrow_kernel<N, T>, dev, G::smem);
     if (st != Q4A_OK) return st;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -458,10 +415,37 @@ q4a_status launch_narrow(const Fp8Gemm& g, int dev, int sms, cudaStream_t stream
 
 }  // namespace
 
+// e4m3 rows [rows][in_dim] in boxes of 128 bytes x box_rows.
+CUresult fp8_rows_map(CUtensorMap* m, const uint8_t* base, int64_t rows, int64_t in_dim, int box_rows) {
+    const cuuint64_t dims[2] = {(cuuint64_t)in_dim, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)in_dim};
+    const cuuint32_t box[2] = {(cuuint32_t)kFp8Block, (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1u, 1u};
+    return encode_tiled_cached(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box, estr,
+                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+q4a_status fp8_sm_count(int* dev, int* sms) {
+    static std::mutex mu;
+    static std::map<int, int> cache;
+    cudaError_t e = cudaGetDevice(dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    std::lock_guard<std::mutex> lock(mu);
+    int& n = cache[*dev];
+    if (n <= 0) {
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, *dev);
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    *sms = n;
+    return Q4A_OK;
+}
+
 q4a_status launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t stream) {
     int dev = 0, sms = 0;
-    const q4a_status st = sm_count(&dev, &sms);
+    const q4a_status st = fp8_sm_count(&dev, &sms);
     if (st != Q4A_OK) return st;
+    if (g.nb > 256) return launch_gemm_fp8_wide(g, stream);
     if (g.q) {
         if (g.nb <= 16) return launch_narrow<16, 2>(g, dev, sms, stream);
         if (g.nb <= 32) return launch_narrow<32, 2>(g, dev, sms, stream);

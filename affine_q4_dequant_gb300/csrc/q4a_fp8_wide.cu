@@ -1,0 +1,466 @@
+// q4a_fp8_wide.cu -- the block-scaled 8-bit product for many activation rows, a contraction:
+// 256 activation rows x 256 weight rows a tile, on a pair of SMs.
+//
+// The activations are the MMA's M and the weights its N, so a TMEM lane is an activation row and a
+// thread's factor for a block of 128 columns is one number, xs[row][k] * ws[k]: an accumulator
+// column costs half a packed fused multiply-add and a share of a TMEM load, nothing else. A block
+// (four tcgen05.mma of 32 columns, 256 x 256) keeps the pair's tensor cores busy for about 512
+// cycles, in which the adding warps of each SM empty the previous block's accumulator (128 x 256
+// fp32): two accumulators fill the TMEM. cta_group::2 lets each SM hold half of the weights' tile:
+// a lone SM would read 48 KB of shared memory a block, 32 KB here.
+//
+// CTA (320 threads; two of them a cluster, one persistent cluster per SM pair):
+//   warp 0      TMA producer of this CTA's 128 activation rows and 128 weight rows of a block,
+//               signalled on the leader's barrier; the rows' and the tile's scales by cp.async
+//   warp 1      allocates TMEM; in the leader issues the MMAs of both CTAs
+//   warps 2..9  add the blocks (thread = activation row, 128 of the 256 columns), then store
+// In the gated form the tile's weight rows are 128 gate and the 128 up rows with the same index,
+// and a thread holds 64 of each.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <string.h>
+
+#include "q4a_fp8.h"
+#include "q4a_internal.h"
+#include "q4a_tcgen05.cuh"
+
+namespace q4a {
+namespace {
+
+constexpr int kWdThreads = 320;
+constexpr int kWdAdd0 = 2, kWdAddWarps = 8;
+constexpr int kWdTile = 128 * 128;                 // bytes of 128 rows of one block
+constexpr int kWdStage = 2 * kWdTile;              // activations, then weights, of one CTA
+constexpr int kWdS = 5;                            // stages
+// Scales of four blocks of a tile: 128 rows', then the tile's two weight blocks'. A slot is reused
+// kWdSL fillings, so at least as many blocks, later: the producer then knows (by its stage) that the
+// MMAs of kWdS blocks ago are done, so that accumulator's previous use, two blocks earlier, has been
+// added.
+constexpr int kWdSL = kWdS + 2;
+constexpr int kWdSlot = (128 + 2) * 16;
+constexpr int kWdBox = 32 * 128;                   // y store box of a warp: 32 rows of 128 bytes
+constexpr int kWdScales = kWdS * kWdStage;
+constexpr int kWdY = (kWdScales + kWdSL * kWdSlot + 1023) / 1024 * 1024;
+constexpr int kWdMax = kWdY + kWdAddWarps * kWdBox;              // gated: rows' maxima, [2][128]
+constexpr int kWdBars = kWdMax + 2 * 128 * 4;      // full[S] empty[S] scale_full[SL] acc_full[2] acc_empty[2]
+constexpr int kWdTmemSlot = kWdBars + (2 * kWdS + kWdSL + 4) * 8;
+constexpr int kWdAbort = kWdTmemSlot + 4;
+constexpr int kWdSmem = kWdAbort + 4 + 1024;
+static_assert(kWdSmem <= 227 * 1024, "shared memory");
+
+struct WideParams {
+    CUtensorMap tmap_w;    // e4m3 [weight rows][in_dim], box 128 bytes x 128 rows, 128-byte swizzle
+    CUtensorMap tmap_x;    // e4m3 [nb][in_dim], the same box
+    CUtensorMap tmap_y;    // y [nb][out_dim], box 128 bytes x 32 rows, 128-byte swizzle (when y_tma)
+    Fp8Gemm g;
+    int32_t nk;            // column blocks
+    int32_t m_tiles, n_tiles;
+    int32_t y_tma;
+    int32_t xs_vec;        // rows of x_scale allow 16-byte copies
+};
+
+__device__ __forceinline__ uint32_t wd_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void wd_cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+}
+// The address of the leader's copy of a shared variable.
+__device__ __forceinline__ uint32_t leader_addr(uint32_t addr) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
+}
+// Tells the leader that an accumulator has been read. The reads are complete (tcgen05.wait::ld) and
+// ordered by the tcgen05 fences, and no other data is handed over: a release at cluster scope
+// would wait for all of the thread's memory traffic, about 1000 cycles a block.
+__device__ __forceinline__ void wd_arrive_leader(uint32_t leader_bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_bar) : "memory");
+}
+
+__device__ __forceinline__ void wd_tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t leader_bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(leader_bar)
+        : "memory");
+}
+// 4 bytes, or zeros where !on.
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const float* src, bool on) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const float* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void wd_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrives on the barrier of both CTAs once the MMAs issued before have completed.
+__device__ __forceinline__ void wd_commit(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void wd_fma2(uint64_t& acc, uint32_t d0, uint32_t d1, uint64_t s) {
+    asm("{\n .reg .b64 d;\n mov.b64 d, {%1, %2};\n fma.rn.f32x2 %0, d, %3, %0;\n}" : "+l"(acc) : "r"(d0), "r"(d1), "l"(s));
+}
+__device__ __forceinline__ float lo(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+
+// Tile t: groups of 8 row tiles pass over all weight tiles, so the pairs at work share both.
+__device__ __forceinline__ void tile_at(const WideParams& p, int t, int64_t& m0, int& nt) {
+    const int per = 8 * p.n_tiles, group = t / per, in = t - group * per;
+    const int rows = p.m_tiles - group * 8 < 8 ? p.m_tiles - group * 8 : 8;
+    m0 = (int64_t)(group * 8 + in % rows) * 256;
+    nt = in / rows;
+}
+
+__device__ __forceinline__ uint32_t pack_y(float a, float b, int type) {
+    if (type == Q4A_F16) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <bool GATED>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
+    wide_kernel(const __grid_constant__ WideParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t base = smem_addr(smem);
+    const uint32_t full = base + kWdBars, empty = full + 8 * kWdS, scale_full = empty + 8 * kWdS;
+    const uint32_t acc_full = scale_full + 8 * kWdSL, acc_empty = acc_full + 16;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kWdTmemSlot);
+    volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + kWdAbort);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)wd_rank();
+    const int pairs = (int)(gridDim.x >> 1), pair = (int)(blockIdx.x >> 1);
+    const int tiles = p.m_tiles * p.n_tiles, nk = p.nk;
+
+    grid_dep_launch();
+    if (threadIdx.x == 0) {
+        prefetch_tensormap(&p.tmap_w);
+        prefetch_tensormap(&p.tmap_x);
+        for (int i = 0; i < kWdS; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < kWdSL; ++i) mbar_init(scale_full + 8 * i, 32);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full + 8 * i, 1);
+            mbar_init(acc_empty + 8 * i, 2 * kWdAddWarps);
+        }
+        *abort_flag = 0u;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(tmem_slot))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    wd_cluster_sync();   // the leader's barriers exist before the peer signals them
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    grid_dep_wait();   // operands, scales and outputs may belong to the previous kernel of the stream
+
+    if (warp == 0) {
+        int i = 0, fill = 0;
+        for (int t = pair; t < tiles; t += pairs) {
+            int64_t m0;
+            int nt;
+            tile_at(p, t, m0, nt);
+            m0 += rank * 128;
+            const int64_t wrow = GATED ? rank * p.g.out_dim + (int64_t)nt * 128 : (int64_t)nt * 256 + rank * 128;
+            // the weight blocks of the tile's two column halves (a half beyond out_dim: any factor)
+            const int64_t wb0 = GATED ? (int64_t)nt : (int64_t)nt * 2;
+            const int64_t wb1 = GATED ? p.g.out_dim / kFp8Block + nt
+                                      : (wb0 + 1 < (p.g.out_dim + 127) / 128 ? wb0 + 1 : wb0);
+            for (int kb = 0; kb < nk; ++kb, ++i) {
+                const int s = i % kWdS;
+                if (i >= kWdS) mbar_wait(empty + 8 * s, (uint32_t)(i / kWdS - 1) & 1u, abort_flag);
+                if (lane == 0) {
+                    if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * kWdStage);
+                    const uint32_t lf = leader_addr(full + 8 * s), at = base + s * kWdStage;
+                    wd_tma_load(at, &p.tmap_x, kb * kFp8Block, (int)m0, lf);
+                    wd_tma_load(at + kWdTile, &p.tmap_w, kb * kFp8Block, (int)wrow, lf);
+                }
+                __syncwarp();
+                if ((kb & 3) == 0) {
+                    // a row's four scales in one copy where it is aligned: a copy touches 32 lines,
+                    // and their queue would hold up the adding warps of this SM quarter
+                    const int sl = fill % kWdSL;
+                    const uint32_t slot = base + kWdScales + sl * kWdSlot;
+                    ++fill;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int64_t r = m0 + 32 * j + lane;
+                        const float* src = p.g.x_scale + (r < p.g.nb ? r * nk + kb : 0);
+                        const uint32_t dst = slot + (uint32_t)(32 * j + lane) * 16u;
+                        if (p.xs_vec) cp_async_16(dst, src, r < p.g.nb);
+                        else
+                            for (int k = 0; k < 4 && kb + k < nk; ++k) cp_async_4(dst + 4u * k, src + (r < p.g.nb ? k : 0), r < p.g.nb);
+                    }
+                    // [block][column half]
+                    if (lane < 8 && kb + (lane >> 1) < nk)
+                        cp_async_4(slot + 2048u + 4u * lane, p.g.w_scale + (lane & 1 ? wb1 : wb0) * nk + kb + (lane >> 1), true);
+                    cp_async_arrive(scale_full + 8 * sl);
+                }
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == 1) {
+        if (rank == 0) {
+            constexpr uint32_t idesc = idesc_f8(256, 256);
+            int i = 0;
+            for (int t = pair; t < tiles; t += pairs) {
+                for (int kb = 0; kb < nk; ++kb, ++i) {
+                    const int s = i % kWdS, buf = i & 1;
+                    mbar_wait(full + 8 * s, (uint32_t)(i / kWdS) & 1u, abort_flag);
+                    if (i >= 2) mbar_wait(acc_empty + 8 * buf, (uint32_t)(i / 2 - 1) & 1u, abort_flag);
+                    __syncwarp();
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t ad = smem_desc(base + s * kWdStage), bd = smem_desc(base + s * kWdStage + kWdTile);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            wd_mma(tmem + (uint32_t)(buf * 256), ad + 2u * k, bd + 2u * k, idesc, (uint32_t)k);
+                        wd_commit(acc_full + 8 * buf);
+                        wd_commit(empty + 8 * s);
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+    } else {
+        const int wg = (warp - kWdAdd0) >> 2, quarter = warp & 3;
+        const int rl = quarter * 32 + lane;                  // row of this CTA's 128
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        // this thread's columns: two spans of 64
+        const int span0 = GATED ? wg * 64 : wg * 128, span1 = GATED ? 128 + wg * 64 : wg * 128 + 64;
+        const uint32_t box = base + kWdY + (uint32_t)(warp - kWdAdd0) * kWdBox;
+        const uint32_t free0 = leader_addr(acc_empty);
+        int i = 0, fill = 0;
+        uint64_t acc[64];
+        for (int t = pair; t < tiles; t += pairs) {
+            int64_t m0;
+            int nt;
+            tile_at(p, t, m0, nt);
+            const int64_t row = m0 + rank * 128 + rl;
+#pragma unroll
+            for (int c = 0; c < 64; ++c) acc[c] = 0;
+            for (int kb = 0; kb < nk; ++kb, ++i) {
+                const int buf = i & 1;
+                if ((kb & 3) == 0) {
+                    mbar_wait(scale_full + 8 * (fill % kWdSL), (uint32_t)(fill / kWdSL) & 1u, abort_flag);
+                    ++fill;
+                }
+                const uint32_t slot = base + kWdScales + (uint32_t)((fill - 1) % kWdSL) * kWdSlot;
+                float xs, w0, w1;
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(xs) : "r"(slot + (uint32_t)rl * 16u + 4u * (kb & 3)));
+                asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(w0), "=f"(w1) : "r"(slot + 2048u + 8u * (kb & 3)));
+                const float f0 = xs * (GATED ? w0 : (wg ? w1 : w0)), f1 = xs * (GATED ? w1 : (wg ? w1 : w0));
+                const uint64_t s0 = pack2(f0, f0), s1 = pack2(f1, f1);
+                mbar_wait(acc_full + 8 * buf, (uint32_t)(i / 2) & 1u, abort_flag);
+                tc_fence_after();
+                const uint32_t at = lanes + (uint32_t)(buf * 256);
+                uint32_t d[2][16];
+                tc_ld16_issue(at + span0, d[0]);
+                tc_ld16_wait(d[0]);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {   // 16 columns a step, the next step's load in flight
+                    if (c < 7) tc_ld16_issue(at + (c + 1 < 4 ? span0 + 16 * (c + 1) : span1 + 16 * (c - 3)), d[(c + 1) & 1]);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) wd_fma2(acc[8 * c + k], d[c & 1][2 * k], d[c & 1][2 * k + 1], c < 4 ? s0 : s1);
+                    if (c < 7) tc_ld16_wait(d[(c + 1) & 1]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) wd_arrive_leader(free0 + 8 * buf);
+            }
+            if (GATED) {
+                float amax = 0.f;
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const float a = gated(lo(acc[c]), lo(acc[32 + c])), b = gated(hi(acc[c]), hi(acc[32 + c]));
+                    acc[c] = pack2(a, b);
+                    amax = fmaxf(amax, fmaxf(fabsf(a), fabsf(b)));
+                }
+                // the two warps of a row quarter share the rows' maxima
+                float* s_max = reinterpret_cast<float*>(smem + kWdMax);
+                s_max[wg * 128 + rl] = amax;
+                asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+                amax = fmaxf(amax, s_max[(1 - wg) * 128 + rl]);
+                asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+                const float scale = fp8_scale(amax), inv = 1.f / scale;
+                if (row < p.g.nb) {
+                    uint4* q = reinterpret_cast<uint4*>(p.g.q + row * p.g.out_dim + (int64_t)nt * 128 + wg * 64);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint64_t a = acc[8 * c + 2 * k], b = acc[8 * c + 2 * k + 1];
+                            w[k] = e4m3x4(lo(a) * inv, hi(a) * inv, lo(b) * inv, hi(b) * inv);
+                        }
+                        q[c] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    if (wg == 0) p.g.scale[row * (p.g.out_dim / kFp8Block) + nt] = scale;
+                }
+            } else if (p.y_tma) {
+                // 128 bytes of a row at a time through this warp's box (16-byte unit u of row r at
+                // u ^ (r & 7)), rows and columns beyond y clipped by the tensor map
+                const int64_t col0 = (int64_t)nt * 256 + wg * 128, row0 = m0 + rank * 128 + quarter * 32;
+                const bool f32 = p.g.y_type == Q4A_F32;
+                const uint32_t line = box + (uint32_t)lane * 128u, sw = (uint32_t)lane & 7u;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (!f32 && (c & 1)) continue;
+                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    __syncwarp();
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        uint32_t v[4];
+                        if (f32) {
+                            const uint64_t a = acc[16 * c + 2 * u], b = acc[16 * c + 2 * u + 1];
+                            v[0] = (uint32_t)a, v[1] = (uint32_t)(a >> 32), v[2] = (uint32_t)b, v[3] = (uint32_t)(b >> 32);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint64_t a = acc[(16 * c + 4 * u + k) & 63];
+                                v[k] = pack_y(lo(a), hi(a), p.g.y_type);
+                            }
+                        }
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(line + (((uint32_t)u ^ sw) << 4)), "r"(v[0]),
+                                     "r"(v[1]), "r"(v[2]), "r"(v[3])
+                                     : "memory");
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    const int64_t col = col0 + 32 * c;
+                    if (lane == 0 && row0 < p.g.nb && col < p.g.out_dim) tma_store_2d(&p.tmap_y, box, (int)col, (int)row0);
+                }
+            } else if (row < p.g.nb) {
+                const int64_t col0 = (int64_t)nt * 256 + wg * 128;
+#pragma unroll
+                for (int c = 0; c < 128; ++c) {
+                    const float f = c & 1 ? hi(acc[c / 2]) : lo(acc[c / 2]);
+                    if (col0 + c < p.g.out_dim) {
+                        const int64_t at = row * p.g.out_dim + col0 + c;
+                        if (p.g.y_type == Q4A_F32) static_cast<float*>(p.g.y)[at] = f;
+                        else if (p.g.y_type == Q4A_F16) static_cast<__half*>(p.g.y)[at] = __float2half_rn(f);
+                        else static_cast<__nv_bfloat16*>(p.g.y)[at] = __float2bfloat16_rn(f);
+                    }
+                }
+            }
+        }
+        if (lane == 0) bulk_wait_all();   // no CTA exits while its y stores read shared memory
+    }
+
+    // after a give-up no one has waited for the last copies and MMAs: they may not outlive the CTA
+    if (*abort_flag && warp == 1 && rank == 0) {
+        int n = 0;
+        for (int t = pair; t < tiles; t += pairs) n += nk;
+        for (int i = n < kWdS ? 0 : n - kWdS; i < n; ++i) mbar_drain(full + 8 * (i % kWdS), (uint32_t)(i / kWdS) & 1u);
+        for (int i = n < 2 ? 0 : n - 2; i < n; ++i) mbar_drain(acc_full + 8 * (i & 1), (uint32_t)(i / 2) & 1u);
+    }
+    __syncwarp();
+    tc_fence_before();
+    wd_cluster_sync();
+    tc_fence_after();
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+}  // namespace
+
+q4a_status launch_gemm_fp8_wide(const Fp8Gemm& g, cudaStream_t stream) {
+    int dev = 0, sms = 0;
+    q4a_status st = fp8_sm_count(&dev, &sms);
+    if (st != Q4A_OK) return st;
+    const bool gated_form = g.q != nullptr;
+    WideParams p;
+    memset(&p, 0, sizeof(p));
+    CUresult r = fp8_rows_map(&p.tmap_w, g.w, gated_form ? 2 * g.out_dim : g.out_dim, g.in_dim, 128);
+    if (r != CUDA_SUCCESS) return cuda_fail_drv(r);
+    r = fp8_rows_map(&p.tmap_x, g.x, g.nb, g.in_dim, 128);
+    if (r != CUDA_SUCCESS) return cuda_fail_drv(r);
+    p.g = g;
+    p.nk = (int32_t)((g.in_dim + kFp8Block - 1) / kFp8Block);
+    const int64_t m_tiles = (g.nb + 255) / 256;
+    const int64_t n_tiles = gated_form ? g.out_dim / 128 : (g.out_dim + 255) / 256;
+    // the blocks of one pair are counted in 32 bits
+    if (m_tiles * n_tiles * p.nk > ((int64_t)1 << 31) - 1) return Q4A_ERR_UNSUPPORTED;
+    p.m_tiles = (int32_t)m_tiles;
+    p.n_tiles = (int32_t)n_tiles;
+    p.xs_vec = p.nk % 4 == 0 && reinterpret_cast<uintptr_t>(g.x_scale) % 16 == 0;
+    const int64_t size = fp8_type_bytes(g.y_type);
+    // y through tensor stores: 16-byte rows, and a tensor that holds a box
+    if (!gated_form && g.out_dim * size % 16 == 0 && reinterpret_cast<uintptr_t>(g.y) % 16 == 0 && g.nb >= 32 &&
+        g.out_dim * size >= 128) {
+        const cuuint64_t dims[2] = {(cuuint64_t)g.out_dim, (cuuint64_t)g.nb};
+        const cuuint64_t strides[1] = {(cuuint64_t)(g.out_dim * size)};
+        const cuuint32_t box[2] = {(cuuint32_t)(128 / size), 32u};
+        const cuuint32_t estr[2] = {1u, 1u};
+        const CUtensorMapDataType dt = g.y_type == Q4A_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                       : g.y_type == Q4A_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+        r = encode_tiled_cached(&p.tmap_y, dt, 2, g.y, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (r != CUDA_SUCCESS) return cuda_fail_drv(r);
+        p.y_tma = 1;
+    }
+    auto kernel = gated_form ? wide_kernel<true> : wide_kernel<false>;
+    st = fp8_allow_smem(kernel, dev, kWdSmem);
+    if (st != Q4A_OK) return st;
+    const int64_t tiles = m_tiles * n_tiles, pairs = sms / 2;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)), 1, 1);
+    cfg.blockDim = dim3(kWdThreads, 1, 1);
+    cfg.dynamicSmemBytes = kWdSmem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+    return e == cudaSuccess ? Q4A_OK : cuda_fail(e);
+}
+
+q4a_status read_and_clear_fp8_wide_error(uint32_t* word) {
+    uint32_t v = 0, zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_device_error, sizeof(v));
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (v) {
+        e = cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero));
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    *word = v;
+    return Q4A_OK;
+}
+
+}  // namespace q4a
