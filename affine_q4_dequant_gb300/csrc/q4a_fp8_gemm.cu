@@ -108,27 +108,28 @@ __device__ __forceinline__ float4 lds_f4(uint32_t addr) {
     return v;
 }
 
-// acc (two fp32) += d * s, element by element.
-__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t d0, uint32_t d1, uint64_t s) {
-    asm("{\n .reg .b64 d;\n mov.b64 d, {%1, %2};\n fma.rn.f32x2 %0, d, %3, %0;\n}" : "+l"(acc) : "r"(d0), "r"(d1), "l"(s));
+__device__ __forceinline__ void sts_f32(uint32_t addr, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
-__device__ __forceinline__ void lds_u64x2(uint32_t addr, uint64_t& a, uint64_t& b) {
-    asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr));
+
+// acc (two fp32) += d * s, element by element.
+__device__ __forceinline__ void fma2(float2& acc, uint32_t d0, uint32_t d1, float2 s) {
+    acc = __ffma2_rn(make_float2(__uint_as_float(d0), __uint_as_float(d1)), s, acc);
 }
 
 // acc[0..CPT) += (accumulator columns) * (their factors in shared memory). The next columns' TMEM
 // load is in flight while the current ones are added.
 template <int CPT>
-__device__ __forceinline__ void add_block(uint64_t (&acc)[CPT / 2], uint32_t taddr, uint32_t saddr) {
+__device__ __forceinline__ void add_block(float2 (&acc)[CPT / 2], uint32_t taddr, uint32_t saddr) {
     if constexpr (CPT == 8) {
         uint32_t d[8];
         tc_ld8_issue(taddr, d);
-        uint64_t s[4];
-        lds_u64x2(saddr, s[0], s[1]);
-        lds_u64x2(saddr + 16, s[2], s[3]);
+        const float4 s0 = lds_f4(saddr), s1 = lds_f4(saddr + 16);
         tc_ld8_wait(d);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) fma2(acc[i], d[2 * i], d[2 * i + 1], s[i]);
+        fma2(acc[0], d[0], d[1], make_float2(s0.x, s0.y));
+        fma2(acc[1], d[2], d[3], make_float2(s0.z, s0.w));
+        fma2(acc[2], d[4], d[5], make_float2(s1.x, s1.y));
+        fma2(acc[3], d[6], d[7], make_float2(s1.z, s1.w));
     } else {
         uint32_t d[2][16];
         tc_ld16_issue(taddr, d[0]);
@@ -138,10 +139,9 @@ __device__ __forceinline__ void add_block(uint64_t (&acc)[CPT / 2], uint32_t tad
             if (c + 1 < CPT / 16) tc_ld16_issue(taddr + 16 * (c + 1), d[(c + 1) & 1]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint64_t s0, s1;
-                lds_u64x2(saddr + (uint32_t)(16 * c + 4 * i) * 4u, s0, s1);
-                fma2(acc[8 * c + 2 * i], d[c & 1][4 * i], d[c & 1][4 * i + 1], s0);
-                fma2(acc[8 * c + 2 * i + 1], d[c & 1][4 * i + 2], d[c & 1][4 * i + 3], s1);
+                const float4 s = lds_f4(saddr + (uint32_t)(16 * c + 4 * i) * 4u);
+                fma2(acc[8 * c + 2 * i], d[c & 1][4 * i], d[c & 1][4 * i + 1], make_float2(s.x, s.y));
+                fma2(acc[8 * c + 2 * i + 1], d[c & 1][4 * i + 2], d[c & 1][4 * i + 3], make_float2(s.z, s.w));
             }
             if (c + 1 < CPT / 16) tc_ld16_wait(d[(c + 1) & 1]);
         }
@@ -284,9 +284,9 @@ __global__ void __launch_bounds__(kNwThreads, Narrow<N, T>::R) narrow_kernel(con
         const int wg = (warp - kNwAdd0) >> 2, quarter = warp & 3;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(wg * CPT);
         const uint32_t sbase = smem_addr(scales) + (uint32_t)(wg * CPT) * 4u;
-        uint64_t acc[CPT / 2];
+        float2 acc[CPT / 2];
 #pragma unroll
-        for (int c = 0; c < CPT / 2; ++c) acc[c] = 0;
+        for (int c = 0; c < CPT / 2; ++c) acc[c] = make_float2(0.f, 0.f);
         for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
             const int buf = i % AB;
             mbar_wait(smem_addr(scale_full + buf), (uint32_t)(i / AB) & 1u, abort_flag);
@@ -301,9 +301,8 @@ __global__ void __launch_bounds__(kNwThreads, Narrow<N, T>::R) narrow_kernel(con
         const uint32_t part = smem_addr(smem + G::ring) + (uint32_t)((wg * CPT) * 128 + quarter * 32 + lane) * 4u;
 #pragma unroll
         for (int c = 0; c < CPT / 2; ++c) {
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(part + (uint32_t)(2 * c) * 512u), "r"((uint32_t)acc[c]) : "memory");
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(part + (uint32_t)(2 * c + 1) * 512u), "r"((uint32_t)(acc[c] >> 32))
-                         : "memory");
+            sts_f32(part + (uint32_t)(2 * c) * 512u, acc[c].x);
+            sts_f32(part + (uint32_t)(2 * c + 1) * 512u, acc[c].y);
         }
     }
 

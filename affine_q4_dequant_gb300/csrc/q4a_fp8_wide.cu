@@ -115,17 +115,6 @@ __device__ __forceinline__ void wd_commit(uint32_t bar) {
         : "memory");
 }
 
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void wd_fma2(uint64_t& acc, uint32_t d0, uint32_t d1, uint64_t s) {
-    asm("{\n .reg .b64 d;\n mov.b64 d, {%1, %2};\n fma.rn.f32x2 %0, d, %3, %0;\n}" : "+l"(acc) : "r"(d0), "r"(d1), "l"(s));
-}
-__device__ __forceinline__ float lo(uint64_t v) { return __uint_as_float((uint32_t)v); }
-__device__ __forceinline__ float hi(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
-
 // Tile t: groups of 8 row tiles pass over all weight tiles, so the pairs at work share both.
 __device__ __forceinline__ void tile_at(const WideParams& p, int t, int64_t& m0, int& nt) {
     const int per = 8 * p.n_tiles, group = t / per, in = t - group * per;
@@ -188,7 +177,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
     grid_dep_wait();   // operands, scales and outputs may belong to the previous kernel of the stream
 
     if (warp == 0) {
-        int i = 0, fill = 0;
+        int s = 0, sl = 0;
+        uint32_t s_phase = 1;   // the first use of a stage finds it free
         for (int t = pair; t < tiles; t += pairs) {
             int64_t m0;
             int nt;
@@ -199,9 +189,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
             const int64_t wb0 = GATED ? (int64_t)nt : (int64_t)nt * 2;
             const int64_t wb1 = GATED ? p.g.out_dim / kFp8Block + nt
                                       : (wb0 + 1 < (p.g.out_dim + 127) / 128 ? wb0 + 1 : wb0);
-            for (int kb = 0; kb < nk; ++kb, ++i) {
-                const int s = i % kWdS;
-                if (i >= kWdS) mbar_wait(empty + 8 * s, (uint32_t)(i / kWdS - 1) & 1u, abort_flag);
+            for (int kb = 0; kb < nk; ++kb) {
+                mbar_wait(empty + 8 * s, s_phase, abort_flag);
                 if (lane == 0) {
                     if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * kWdStage);
                     const uint32_t lf = leader_addr(full + 8 * s), at = base + s * kWdStage;
@@ -212,9 +201,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                 if ((kb & 3) == 0) {
                     // a row's four scales in one copy where it is aligned: a copy touches 32 lines,
                     // and their queue would hold up the adding warps of this SM quarter
-                    const int sl = fill % kWdSL;
                     const uint32_t slot = base + kWdScales + sl * kWdSlot;
-                    ++fill;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int64_t r = m0 + 32 * j + lane;
@@ -228,19 +215,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                     if (lane < 8 && kb + (lane >> 1) < nk)
                         cp_async_4(slot + 2048u + 4u * lane, p.g.w_scale + (lane & 1 ? wb1 : wb0) * nk + kb + (lane >> 1), true);
                     cp_async_arrive(scale_full + 8 * sl);
+                    if (++sl == kWdSL) sl = 0;
                 }
+                if (++s == kWdS) s = 0, s_phase ^= 1;
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == 1) {
         if (rank == 0) {
             constexpr uint32_t idesc = idesc_f8(256, 256);
-            int i = 0;
+            int s = 0;
+            uint32_t s_phase = 0, buf = 0, buf_phase = 1;   // the first use of an accumulator finds it free
             for (int t = pair; t < tiles; t += pairs) {
-                for (int kb = 0; kb < nk; ++kb, ++i) {
-                    const int s = i % kWdS, buf = i & 1;
-                    mbar_wait(full + 8 * s, (uint32_t)(i / kWdS) & 1u, abort_flag);
-                    if (i >= 2) mbar_wait(acc_empty + 8 * buf, (uint32_t)(i / 2 - 1) & 1u, abort_flag);
+                for (int kb = 0; kb < nk; ++kb) {
+                    mbar_wait(full + 8 * s, s_phase, abort_flag);
+                    mbar_wait(acc_empty + 8 * buf, buf_phase, abort_flag);
                     __syncwarp();
                     tc_fence_after();
                     if (elect_one()) {
@@ -252,6 +241,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                         wd_commit(empty + 8 * s);
                     }
                     __syncwarp();
+                    if (++s == kWdS) s = 0, s_phase ^= 1;
+                    if ((buf ^= 1) == 0) buf_phase ^= 1;
                 }
             }
         }
@@ -263,27 +254,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
         const int span0 = GATED ? wg * 64 : wg * 128, span1 = GATED ? 128 + wg * 64 : wg * 128 + 64;
         const uint32_t box = base + kWdY + (uint32_t)(warp - kWdAdd0) * kWdBox;
         const uint32_t free0 = leader_addr(acc_empty);
-        int i = 0, fill = 0;
-        uint64_t acc[64];
+        int i = 0, sl = kWdSL - 1;
+        uint32_t sl_phase = 1;
+        float2 acc[64];
         for (int t = pair; t < tiles; t += pairs) {
             int64_t m0;
             int nt;
             tile_at(p, t, m0, nt);
             const int64_t row = m0 + rank * 128 + rl;
 #pragma unroll
-            for (int c = 0; c < 64; ++c) acc[c] = 0;
+            for (int c = 0; c < 64; ++c) acc[c] = make_float2(0.f, 0.f);
             for (int kb = 0; kb < nk; ++kb, ++i) {
                 const int buf = i & 1;
                 if ((kb & 3) == 0) {
-                    mbar_wait(scale_full + 8 * (fill % kWdSL), (uint32_t)(fill / kWdSL) & 1u, abort_flag);
-                    ++fill;
+                    if (++sl == kWdSL) sl = 0, sl_phase ^= 1;
+                    mbar_wait(scale_full + 8 * sl, sl_phase, abort_flag);
                 }
-                const uint32_t slot = base + kWdScales + (uint32_t)((fill - 1) % kWdSL) * kWdSlot;
+                const uint32_t slot = base + kWdScales + (uint32_t)sl * kWdSlot;
                 float xs, w0, w1;
                 asm volatile("ld.shared.f32 %0, [%1];" : "=f"(xs) : "r"(slot + (uint32_t)rl * 16u + 4u * (kb & 3)));
                 asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(w0), "=f"(w1) : "r"(slot + 2048u + 8u * (kb & 3)));
                 const float f0 = xs * (GATED ? w0 : (wg ? w1 : w0)), f1 = xs * (GATED ? w1 : (wg ? w1 : w0));
-                const uint64_t s0 = pack2(f0, f0), s1 = pack2(f1, f1);
+                const float2 s0 = make_float2(f0, f0), s1 = make_float2(f1, f1);
                 mbar_wait(acc_full + 8 * buf, (uint32_t)(i / 2) & 1u, abort_flag);
                 tc_fence_after();
                 const uint32_t at = lanes + (uint32_t)(buf * 256);
@@ -293,20 +285,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {   // 16 columns a step, the next step's load in flight
                     if (c < 7) tc_ld16_issue(at + (c + 1 < 4 ? span0 + 16 * (c + 1) : span1 + 16 * (c - 3)), d[(c + 1) & 1]);
+                    if (c == 7) {   // all read: the next block may overwrite them
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) wd_arrive_leader(free0 + 8 * buf);
+                    }
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) wd_fma2(acc[8 * c + k], d[c & 1][2 * k], d[c & 1][2 * k + 1], c < 4 ? s0 : s1);
+                    for (int k = 0; k < 8; ++k)
+                        acc[8 * c + k] = __ffma2_rn(make_float2(__uint_as_float(d[c & 1][2 * k]),
+                                                                __uint_as_float(d[c & 1][2 * k + 1])),
+                                                    c < 4 ? s0 : s1, acc[8 * c + k]);
                     if (c < 7) tc_ld16_wait(d[(c + 1) & 1]);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) wd_arrive_leader(free0 + 8 * buf);
             }
             if (GATED) {
                 float amax = 0.f;
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
-                    const float a = gated(lo(acc[c]), lo(acc[32 + c])), b = gated(hi(acc[c]), hi(acc[32 + c]));
-                    acc[c] = pack2(a, b);
+                    const float a = gated(acc[c].x, acc[32 + c].x), b = gated(acc[c].y, acc[32 + c].y);
+                    acc[c] = make_float2(a, b);
                     amax = fmaxf(amax, fmaxf(fabsf(a), fabsf(b)));
                 }
                 // the two warps of a row quarter share the rows' maxima
@@ -323,8 +320,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                         uint32_t w[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const uint64_t a = acc[8 * c + 2 * k], b = acc[8 * c + 2 * k + 1];
-                            w[k] = e4m3x4(lo(a) * inv, hi(a) * inv, lo(b) * inv, hi(b) * inv);
+                            const float2 a = acc[8 * c + 2 * k], b = acc[8 * c + 2 * k + 1];
+                            w[k] = e4m3x4(a.x * inv, a.y * inv, b.x * inv, b.y * inv);
                         }
                         q[c] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
@@ -345,13 +342,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                     for (int u = 0; u < 8; ++u) {
                         uint32_t v[4];
                         if (f32) {
-                            const uint64_t a = acc[16 * c + 2 * u], b = acc[16 * c + 2 * u + 1];
-                            v[0] = (uint32_t)a, v[1] = (uint32_t)(a >> 32), v[2] = (uint32_t)b, v[3] = (uint32_t)(b >> 32);
+                            const float2 a = acc[16 * c + 2 * u], b = acc[16 * c + 2 * u + 1];
+                            v[0] = __float_as_uint(a.x), v[1] = __float_as_uint(a.y), v[2] = __float_as_uint(b.x), v[3] = __float_as_uint(b.y);
                         } else {
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                const uint64_t a = acc[(16 * c + 4 * u + k) & 63];
-                                v[k] = pack_y(lo(a), hi(a), p.g.y_type);
+                                const float2 a = acc[(16 * c + 4 * u + k) & 63];
+                                v[k] = pack_y(a.x, a.y, p.g.y_type);
                             }
                         }
                         asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(line + (((uint32_t)u ^ sw) << 4)), "r"(v[0]),
@@ -367,7 +364,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                 const int64_t col0 = (int64_t)nt * 256 + wg * 128;
 #pragma unroll
                 for (int c = 0; c < 128; ++c) {
-                    const float f = c & 1 ? hi(acc[c / 2]) : lo(acc[c / 2]);
+                    const float f = c & 1 ? acc[c / 2].y : acc[c / 2].x;
                     if (col0 + c < p.g.out_dim) {
                         const int64_t at = row * p.g.out_dim + col0 + c;
                         if (p.g.y_type == Q4A_F32) static_cast<float*>(p.g.y)[at] = f;
