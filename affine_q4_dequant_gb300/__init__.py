@@ -115,13 +115,16 @@ def _check(fn: str, status: int) -> None:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+_cuda_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _stream(stream=None) -> int:
     """The cudaStream_t to launch on: the given torch stream, else the current stream of the
     current device (a plain integer handle; the call happens per launch, so it stays cheap)."""
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_cuda_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -138,10 +141,31 @@ _NULL = ctypes.c_void_p(0)
 
 def _ptrs(*specs):
     """Device pointers for specs (tensor, name, dtypes, shape); a spec may be None (a NULL
-    pointer). Every shape is checked first, then dtypes, CUDA residency, contiguity and the
-    device: a mis-shaped buffer would be read or written past its end by the kernels, so it is
-    refused here, before anything launches. (Plain comparisons and C-level tensor queries: this
-    runs on every call.)"""
+    pointer). A mis-shaped buffer would be read or written past its end by the kernels, so it is
+    refused here, before anything launches. This runs on every call: one pass over plain
+    comparisons and C-level tensor queries, and _refuse finds what to say where one fails."""
+    out = []
+    try:
+        dev = _cuda_device()
+        for sp in specs:
+            if sp is None:
+                out.append(_NULL)
+                continue
+            t, _, dtypes, shape = sp
+            if (shape is not None and t.shape != shape) or (dtypes is not None and t.dtype not in dtypes) \
+                    or t.get_device() != dev or not t.is_contiguous():
+                break
+            out.append(t.data_ptr())
+        else:
+            return out
+    except (AttributeError, RuntimeError, AssertionError):   # no tensor, or no CUDA device
+        pass
+    return _refuse(*specs)
+
+
+def _refuse(*specs):
+    """Raises for the first wrong spec: every shape is checked first, then dtypes, CUDA residency,
+    the device and contiguity. Returns the pointers if nothing is wrong."""
     for sp in specs:
         if sp is None:
             continue
@@ -171,12 +195,14 @@ def _ptrs(*specs):
         out.append(t.data_ptr())
     return out
 
+
 def _dims(t: torch.Tensor, name: str, ndim: int = 2):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if t.dim() != ndim:
-        raise ValueError(f"{name}: {t.dim()} dimensions, expected {ndim}")
-    return tuple(int(v) for v in t.shape)
+    shape = tuple(t.shape)
+    if len(shape) != ndim:
+        raise ValueError(f"{name}: {len(shape)} dimensions, expected {ndim}")
+    return shape
 
 
 def _mat(w, s, b, out_dim: int, in_dim: int, wname="w", sname="s", bname="b", code_cols=None):

@@ -54,6 +54,7 @@ q4a_status read_and_clear_gemm_fp8_error(uint32_t* word);   // after a stream sy
 
 // The form for many activation rows (q4a_fp8_wide.cu).
 q4a_status launch_gemm_fp8_wide(const Fp8Gemm& g, cudaStream_t stream);
+bool fp8_wide_tma_y(const Fp8Gemm& g);   // whether its y can leave through tensor stores
 q4a_status read_and_clear_fp8_wide_error(uint32_t* word);
 
 // e4m3 rows [rows][in_dim] in boxes of 128 bytes x box_rows, 128-byte swizzle.

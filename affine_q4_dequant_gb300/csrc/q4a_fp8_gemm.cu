@@ -24,6 +24,7 @@
 
 #include <string.h>
 
+#include <array>
 #include <map>
 #include <mutex>
 
@@ -41,6 +42,17 @@ constexpr int kNwAddWarps = 8;
 constexpr int kNwScaleWarp = kNwAdd0 + kNwAddWarps;
 constexpr int kNwTile = 128 * 128;     // bytes of 128 rows of one block
 constexpr int kNwMaxCluster = 8;
+
+// Constants of the launch's choice, us on a GB300, fitted to sweeps over tile and cluster sizes
+// (graphs of back-to-back launches; the choice is within 10% of the best of each sweep):
+//   4096 -> 12288, 1 row    N 16, C 1 / 2 / 3 / 4: 12.9 / 11.4 / 11.1 / 14.0
+//   12288 -> 4096, 128 rows N 128, C 3 / 4: 17.1 / 14.9; N 64, C 4: 17.2; wide: 40.8
+//   656 -> 2050, 333 rows   N 128, C 1 / 2: 6.3 / 7.0; N 64, C 1 / 2 / 3: 7.0 / 6.5 / 9.3
+//   gated 4096 -> 6144      8 rows, N 16, C 3 / 5 / 6: 12.9 / 12.8 / 17.8;
+//                           64 rows, N 64, C 1 / 2: 19.2 / 14.3; N 32, C 3: 15.6; wide: 17.7
+//   4096 -> 12288           wide, 256 / 512 / 1024 rows: 18.1 / 31.2 / 45.0; N 128: 28 and more
+constexpr float kNwBytesPerUs = 9.0e6f, kNwFixedUs = 3.2f, kNwRowUs = 0.006f, kNwSplitUs = 1.0f;
+constexpr float kWdFixedUs = 2.8f, kWdTileUs = 1.2f, kWdScalarUs = 8.f, kWdBlockUs = 0.40f;
 
 constexpr int pow2_at_least(int v) {
     int p = 32;
@@ -187,7 +199,7 @@ __global__ void __launch_bounds__(kNwThreads, Narrow<N, T>::R) narrow_kernel(con
         *abort_flag = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 1) tc_alloc(smem_addr(tmem_slot), G::tmem_cols);
+    if (warp == 1) tc_alloc_n<G::tmem_cols>(smem_addr(tmem_slot));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -311,7 +323,7 @@ __global__ void __launch_bounds__(kNwThreads, Narrow<N, T>::R) narrow_kernel(con
     if (C > 1) nw_cluster_sync();
     else __syncthreads();
     tc_fence_after();
-    if (warp == 1) tc_dealloc(tmem, G::tmem_cols);
+    if (warp == 1) tc_dealloc_n<G::tmem_cols>(tmem);
 
     // A warp takes an activation row, a lane 4 of its 128 outputs; the ranks share the rows.
     const uint32_t ring = smem_addr(smem + G::ring) + (uint32_t)lane * 16u;
@@ -372,8 +384,73 @@ __global__ void __launch_bounds__(kNwThreads, Narrow<N, T>::R) narrow_kernel(con
 
 // ---- host side ---------------------------------------------------------------------------
 
+// Stands for narrow_kernel in occupancy queries (it is never launched): for a kernel that allocates
+// TMEM the query answers one CTA per SM whatever it allocates, where two of these run.
+__global__ void __launch_bounds__(kNwThreads) narrow_shape_kernel() {}
+
+// Clusters of C CTAs that run at once, C = 1..kNwMaxCluster (a cluster stays in one group of SMs, so
+// odd sizes leave some idle). Asked once per kernel and device.
 template <int N, int T>
-q4a_status launch_narrow(const Fp8Gemm& g, int dev, int sms, cudaStream_t stream) {
+q4a_status narrow_slots(int dev, const int** out) {
+    using G = Narrow<N, T>;
+    static std::mutex mu;
+    static std::map<int, std::array<int, kNwMaxCluster + 1>> cache;
+    std::lock_guard<std::mutex> lock(mu);
+    auto& slots = cache[dev];
+    if (slots[1] <= 0) {
+        q4a_status st = fp8_allow_smem(narrow_kernel<N, T>, dev, G::smem);
+        if (st == Q4A_OK) st = fp8_allow_smem(narrow_shape_kernel, dev, 227 * 1024);
+        if (st != Q4A_OK) return st;
+        for (int c = kNwMaxCluster; c >= 1; --c) {
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = (unsigned)c;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.gridDim = dim3((unsigned)c, 1, 1);
+            cfg.blockDim = dim3(kNwThreads, 1, 1);
+            cfg.dynamicSmemBytes = G::R == 1 ? 227 * 1024 : 113 * 1024;   // R CTAs an SM
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            const cudaError_t e = cudaOccupancyMaxActiveClusters(&slots[c], narrow_shape_kernel, &cfg);
+            if (e != cudaSuccess) return cuda_fail(e);
+        }
+    }
+    *out = slots.data();
+    return Q4A_OK;
+}
+
+// A launch and its estimated time in us.
+struct Fp8Plan {
+    int n = 0;         // activation rows of a tile: the narrow kernel; 0: the wide one
+    int cluster = 1;
+    float us = 0.f;
+};
+
+// The narrow kernel with N activation rows a tile, at its best cluster size. A block costs a CTA at
+// least `lat` us (the memory's latency over the ring's stages, or the sums) and its share of the rate
+// at which the L2 and HBM feed all CTAs.
+template <int N, int T>
+q4a_status plan_narrow(const Fp8Gemm& g, int dev, float lat, Fp8Plan* best) {
+    const int* slots = nullptr;
+    const q4a_status st = narrow_slots<N, T>(dev, &slots);
+    if (st != Q4A_OK) return st;
+    const int64_t nk = (g.in_dim + kFp8Block - 1) / kFp8Block;
+    const int64_t tiles = (g.out_dim + 127) / 128 * ((g.nb + N - 1) / N);
+    for (int c = 1; c <= kNwMaxCluster && c <= nk; ++c) {
+        if (slots[c] <= 0) continue;
+        const int64_t waves = (tiles + slots[c] - 1) / slots[c];
+        const float running = (float)((tiles < slots[c] ? tiles : slots[c]) * c);
+        const float feed = running * (float)Narrow<N, T>::stage / kNwBytesPerUs;
+        const float us = kNwFixedUs + kNwRowUs * (float)(T * N) + (c > 1 ? kNwSplitUs : 0.f) +
+                         (float)waves * ((float)((nk + c - 1) / c) * (lat > feed ? lat : feed)) + (float)(waves - 1);
+        if (best->us == 0.f || us < best->us) *best = {N, c, us};
+    }
+    return Q4A_OK;
+}
+
+template <int N, int T>
+q4a_status launch_narrow(const Fp8Gemm& g, int cluster, cudaStream_t stream) {
     using G = Narrow<N, T>;
     NarrowParams p;
     memset(&p, 0, sizeof(p));
@@ -384,30 +461,24 @@ q4a_status launch_narrow(const Fp8Gemm& g, int dev, int sms, cudaStream_t stream
     p.g = g;
     p.nk = (int32_t)((g.in_dim + kFp8Block - 1) / kFp8Block);
     p.n_tiles = (int32_t)((g.nb + N - 1) / N);
+    p.cluster = cluster;
     const int64_t size = fp8_type_bytes(g.y_type);
     p.y_vec = g.out_dim % 4 == 0 && reinterpret_cast<uintptr_t>(g.y) % (4 * size) == 0;
-    const int64_t tiles = (g.out_dim + 127) / 128 * p.n_tiles;
-    int64_t C = (int64_t)sms * G::R / tiles;   // as many CTAs as run at once
-    C = C > kNwMaxCluster ? kNwMaxCluster : C;
-    C = C > p.nk ? p.nk : C;
-    C = C < 1 ? 1 : C;
-    p.cluster = (int32_t)C;
-    if (tiles * C > ((int64_t)1 << 31) - 1) return Q4A_ERR_UNSUPPORTED;
-    const q4a_status st = fp8_allow_smem(narrow_kernel<N, T>, dev, G::smem);
-    if (st != Q4A_OK) return st;
+    const int64_t ctas = (g.out_dim + 127) / 128 * p.n_tiles * cluster;
+    if (ctas > ((int64_t)1 << 31) - 1) return Q4A_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)C;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)(tiles * C), 1, 1);
+    cfg.gridDim = dim3((unsigned)ctas, 1, 1);
     cfg.blockDim = dim3(kNwThreads, 1, 1);
     cfg.dynamicSmemBytes = G::smem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = C > 1 ? 2 : 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, narrow_kernel<N, T>, p);
     return e == cudaSuccess ? Q4A_OK : cuda_fail(e);
 }
@@ -440,22 +511,37 @@ q4a_status fp8_sm_count(int* dev, int* sms) {
     return Q4A_OK;
 }
 
+// The kernel, tile and split with the least estimated time. Tiles of up to twice the rows there are
+// and down to an eighth of them are looked at.
 q4a_status launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t stream) {
     int dev = 0, sms = 0;
-    const q4a_status st = fp8_sm_count(&dev, &sms);
+    q4a_status st = fp8_sm_count(&dev, &sms);
     if (st != Q4A_OK) return st;
-    if (g.nb > 256) return launch_gemm_fp8_wide(g, stream);
-    if (g.q) {
-        if (g.nb <= 16) return launch_narrow<16, 2>(g, dev, sms, stream);
-        if (g.nb <= 32) return launch_narrow<32, 2>(g, dev, sms, stream);
-        if (g.nb <= 64) return launch_narrow<64, 2>(g, dev, sms, stream);
-        return launch_narrow<128, 2>(g, dev, sms, stream);
+    Fp8Plan plan;
+    const bool gated_form = g.q != nullptr;
+    auto consider = [&](int n) { return st == Q4A_OK && (n == 16 || g.nb > n / 2) && (n == 128 || g.nb <= 8 * n); };
+    if (consider(16)) st = gated_form ? plan_narrow<16, 2>(g, dev, 0.45f, &plan) : plan_narrow<16, 1>(g, dev, 0.29f, &plan);
+    if (consider(32)) st = gated_form ? plan_narrow<32, 2>(g, dev, 0.6f, &plan) : plan_narrow<32, 1>(g, dev, 0.30f, &plan);
+    if (consider(64)) st = gated_form ? plan_narrow<64, 2>(g, dev, 0.45f, &plan) : plan_narrow<64, 1>(g, dev, 0.43f, &plan);
+    if (consider(128)) st = gated_form ? plan_narrow<128, 2>(g, dev, 0.8f, &plan) : plan_narrow<128, 1>(g, dev, 0.4f, &plan);
+    if (st != Q4A_OK) return st;
+    {
+        const int64_t nk = (g.in_dim + kFp8Block - 1) / kFp8Block;
+        const int64_t tiles = (g.nb + 255) / 256 * (gated_form ? g.out_dim / 128 : (g.out_dim + 255) / 256);
+        const float waves = (float)((tiles + sms / 2 - 1) / (sms / 2));
+        const float tile = kWdTileUs + (gated_form || fp8_wide_tma_y(g) ? 0.f : kWdScalarUs) + kWdBlockUs * (float)nk;
+        if (kWdFixedUs + waves * tile < plan.us) return launch_gemm_fp8_wide(g, stream);
     }
-    if (g.nb <= 16) return launch_narrow<16, 1>(g, dev, sms, stream);
-    if (g.nb <= 32) return launch_narrow<32, 1>(g, dev, sms, stream);
-    if (g.nb <= 64) return launch_narrow<64, 1>(g, dev, sms, stream);
-    if (g.nb <= 128) return launch_narrow<128, 1>(g, dev, sms, stream);
-    return launch_narrow<256, 1>(g, dev, sms, stream);
+    if (gated_form) {
+        if (plan.n == 16) return launch_narrow<16, 2>(g, plan.cluster, stream);
+        if (plan.n == 32) return launch_narrow<32, 2>(g, plan.cluster, stream);
+        if (plan.n == 64) return launch_narrow<64, 2>(g, plan.cluster, stream);
+        return launch_narrow<128, 2>(g, plan.cluster, stream);
+    }
+    if (plan.n == 16) return launch_narrow<16, 1>(g, plan.cluster, stream);
+    if (plan.n == 32) return launch_narrow<32, 1>(g, plan.cluster, stream);
+    if (plan.n == 64) return launch_narrow<64, 1>(g, plan.cluster, stream);
+    return launch_narrow<128, 1>(g, plan.cluster, stream);
 }
 
 q4a_status read_and_clear_gemm_fp8_error(uint32_t* word) {

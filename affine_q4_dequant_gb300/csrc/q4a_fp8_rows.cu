@@ -187,48 +187,120 @@ q4a_status launch_rows_x(const Fp8Norm& n, cudaStream_t stream) {
     return launch_rows_typed<XT, __nv_bfloat16, true, true>(n, stream);
 }
 
-// One CTA per 128 x 128 block, two threads a row, one 64-input group each: W = fma(s, q, b) for the
-// block's maximum, then again for the codes.
+// Packed 4-bit weights to 8-bit blocks. A CTA takes 128 rows x 256 columns (two blocks); a warp 16
+// rows, 4 at a time, 8 lanes a row; a lane 32 codes (16 bytes), half of a 64-input group.
+//
+// Reading 0.56 and writing 1 byte a weight leaves an SM's 128 lanes about 8 instructions a weight at
+// the HBM rate, so neither pass works on single weights. W is monotonic in the code (so is the
+// rounded multiply-add): a group's largest magnitude is at its smallest or largest code, found on
+// pairs of codes where they lie in the packed word. And a group has 16 possible results: its two
+// lanes round 8 each to e4m3, and a code becomes its byte by permutes over that table.
+constexpr int kDqCols = 256;
+
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Smallest and largest code of four packed words.
+__device__ __forceinline__ void code_range(const uint4& q, uint32_t& lo, uint32_t& hi) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {   // field f of both halves of every word, in place
+        const uint32_t m = 0x000F000Fu << (4 * f);
+        h[f] = max2(max2(w[0] & m, w[1] & m), max2(w[2] & m, w[3] & m)) >> (4 * f);
+        l[f] = min2(min2(w[0] & m, w[1] & m), min2(w[2] & m, w[3] & m)) >> (4 * f);
+    }
+    const uint32_t a = max2(max2(h[0], h[1]), max2(h[2], h[3])), b = min2(min2(l[0], l[1]), min2(l[2], l[3]));
+    hi = max(a & 0xFFFFu, a >> 16);
+    lo = min(b & 0xFFFFu, b >> 16);
+}
+
+// The bytes of codes 0..3 of a packed half word, from the tables of codes 0..7 (t0, t1) and 8..15
+// (t2, t3): a permute takes a byte by three bits, and the fourth chooses between the two.
+__device__ __forceinline__ uint32_t table_bytes(uint32_t low3, uint32_t bit3, uint32_t t0, uint32_t t1, uint32_t t2,
+                                                uint32_t t3) {
+    const uint32_t a = __byte_perm(t0, t1, low3), b = __byte_perm(t2, t3, low3);
+    const uint32_t m = __byte_perm(0x0000FF00u, 0u, bit3);
+    return (a & ~m) | (b & m);
+}
+
 __global__ void __launch_bounds__(256)
     dequant_fp8_kernel(uint8_t* __restrict__ w8, float* __restrict__ w_scale, const uint8_t* __restrict__ w,
                        const uint16_t* __restrict__ s, const uint16_t* __restrict__ b, int64_t rows, int64_t in_dim) {
-    __shared__ float s_max[8];
+    __shared__ float s_max[2][8];
     grid_dep_wait();
     grid_dep_launch();
-    const int64_t nblk = (in_dim + kFp8Block - 1) / kFp8Block;
-    const int64_t kb = blockIdx.x % nblk, rb = blockIdx.x / nblk;
-    const int64_t row = rb * kFp8Block + (threadIdx.x >> 1);
-    const int64_t col = kb * kFp8Block + (threadIdx.x & 1) * kGroup;
-    const bool on = row < rows && col < in_dim;
-    uint32_t word[8] = {};
-    float sv = 0.f, bv = 0.f, amax = 0.f;
-    if (on) {
-        const uint4* src = reinterpret_cast<const uint4*>(w + row * (in_dim / 2) + col / 2);
-        const uint4 a = src[0], c = src[1];
-        word[0] = a.x, word[1] = a.y, word[2] = a.z, word[3] = a.w;
-        word[4] = c.x, word[5] = c.y, word[6] = c.z, word[7] = c.w;
-        sv = bf16_to_f32(s[row * (in_dim / kGroup) + col / kGroup]);
-        bv = bf16_to_f32(b[row * (in_dim / kGroup) + col / kGroup]);
+    const int64_t groups = in_dim / kGroup, nblk = (in_dim + kFp8Block - 1) / kFp8Block;
+    const int64_t tiles = (in_dim + kDqCols - 1) / kDqCols;
+    const int64_t rb = blockIdx.x / tiles, ct = blockIdx.x - rb * tiles;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = lane & 7;
+    const int64_t col = ct * kDqCols + part * 32, row0 = rb * kFp8Block + warp * 16 + (lane >> 3);
+    const bool col_on = col < in_dim;
+    uint4 q[4];
+    uint16_t sb[4], bb[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(fmaf(sv, (float)((word[i] >> (4 * k)) & 15u), bv)));
+    for (int i = 0; i < 4; ++i) {
+        const int64_t row = row0 + 4 * i;
+        const bool on = col_on && row < rows;
+        q[i] = on ? ld_nc_16(w + row * (in_dim / 2) + col / 2) : make_uint4(0, 0, 0, 0);
+        sb[i] = on ? __ldg(s + row * groups + col / kGroup) : (uint16_t)0;
+        bb[i] = on ? __ldg(b + row * groups + col / kGroup) : (uint16_t)0;
     }
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = amax;
-    __syncthreads();
-    amax = 0.f;
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, s_max[i]);
-    const float scale = fp8_scale(amax), inv = 1.f / scale;
-    if (threadIdx.x == 0) w_scale[rb * nblk + kb] = scale;
-    if (!on) return;
-    uint2* dst = reinterpret_cast<uint2*>(w8 + row * in_dim + col);
+    float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
+        uint32_t lo, hi;
+        code_range(q[i], lo, hi);
+        const float sv = bf16_to_f32(sb[i]), bv = bf16_to_f32(bb[i]);
+        amax = fmaxf(amax, fmaxf(fabsf(fmaf(sv, (float)lo, bv)), fabsf(fmaf(sv, (float)hi, bv))));
+    }
+    // lanes of a block: 4 of a row's 8, in all 4 rows
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 8));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
+    if (lane == 0) s_max[0][warp] = amax;
+    if (lane == 4) s_max[1][warp] = amax;
+    __syncthreads();
+    const int blk = part >> 2;
+    amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, s_max[blk][i]);
+    const float scale = fp8_scale(amax), inv = 1.f / scale;
+    if (warp == 0 && (lane == 0 || lane == 4) && col_on) w_scale[rb * nblk + 2 * ct + blk] = scale;
+    const float first = (float)((lane & 1) * 8);   // this lane's half of the group's table
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float sv = bf16_to_f32(sb[i]), bv = bf16_to_f32(bb[i]);
         float v[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = fmaf(sv, (float)((word[i] >> (4 * k)) & 15u), bv) * inv;
-        dst[i] = make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+        for (int k = 0; k < 8; ++k) v[k] = fmaf(sv, first + (float)k, bv) * inv;
+        const uint32_t m0 = e4m3x4(v[0], v[1], v[2], v[3]), m1 = e4m3x4(v[4], v[5], v[6], v[7]);
+        const uint32_t o0 = __shfl_xor_sync(0xffffffffu, m0, 1), o1 = __shfl_xor_sync(0xffffffffu, m1, 1);
+        const bool odd = lane & 1;
+        const uint32_t t0 = odd ? o0 : m0, t1 = odd ? o1 : m1, t2 = odd ? m0 : o0, t3 = odd ? m1 : o1;
+        const uint32_t word[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+        uint32_t out[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t low3 = word[k] & 0x77777777u, bit3 = (word[k] >> 3) & 0x11111111u;
+            out[2 * k] = table_bytes(low3, bit3, t0, t1, t2, t3);
+            out[2 * k + 1] = table_bytes(low3 >> 16, bit3 >> 16, t0, t1, t2, t3);
+        }
+        const int64_t row = row0 + 4 * i;
+        if (col_on && row < rows) {
+            uint4* dst = reinterpret_cast<uint4*>(w8 + row * in_dim + col);
+            dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+            dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+        }
     }
 }
 
@@ -242,7 +314,7 @@ q4a_status launch_fp8_rows(const Fp8Norm& n, cudaStream_t stream) {
 
 q4a_status launch_dequant_fp8(uint8_t* w8, float* w_scale, const uint8_t* w, const uint16_t* s, const uint16_t* b,
                               int64_t rows, int64_t in_dim, cudaStream_t stream) {
-    const int64_t blocks = (rows + kFp8Block - 1) / kFp8Block * ((in_dim + kFp8Block - 1) / kFp8Block);
+    const int64_t blocks = (rows + kFp8Block - 1) / kFp8Block * ((in_dim + kDqCols - 1) / kDqCols);
     if (blocks > ((int64_t)1 << 31) - 1) return Q4A_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];

@@ -52,11 +52,10 @@ static_assert(kWdSmem <= 227 * 1024, "shared memory");
 struct WideParams {
     CUtensorMap tmap_w;    // e4m3 [weight rows][in_dim], box 128 bytes x 128 rows, 128-byte swizzle
     CUtensorMap tmap_x;    // e4m3 [nb][in_dim], the same box
-    CUtensorMap tmap_y;    // y [nb][out_dim], box 128 bytes x 32 rows, 128-byte swizzle (when y_tma)
+    CUtensorMap tmap_y;    // y [nb][out_dim], box 128 bytes x 32 rows, 128-byte swizzle (kernels with TMA_Y)
     Fp8Gemm g;
     int32_t nk;            // column blocks
     int32_t m_tiles, n_tiles;
-    int32_t y_tma;
     int32_t xs_vec;        // rows of x_scale allow 16-byte copies
 };
 
@@ -115,6 +114,10 @@ __device__ __forceinline__ void wd_commit(uint32_t bar) {
         : "memory");
 }
 
+__device__ __forceinline__ void sts_f32(uint32_t addr, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
 // Tile t: groups of 8 row tiles pass over all weight tiles, so the pairs at work share both.
 __device__ __forceinline__ void tile_at(const WideParams& p, int t, int64_t& m0, int& nt) {
     const int per = 8 * p.n_tiles, group = t / per, in = t - group * per;
@@ -132,7 +135,8 @@ __device__ __forceinline__ uint32_t pack_y(float a, float b, int type) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <bool GATED>
+// TMA_Y: y leaves through shared memory and tensor stores.
+template <bool GATED, bool TMA_Y>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
     wide_kernel(const __grid_constant__ WideParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -327,7 +331,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                     }
                     if (wg == 0) p.g.scale[row * (p.g.out_dim / kFp8Block) + nt] = scale;
                 }
-            } else if (p.y_tma) {
+            } else if (TMA_Y) {
                 // 128 bytes of a row at a time through this warp's box (16-byte unit u of row r at
                 // u ^ (r & 7)), rows and columns beyond y clipped by the tensor map
                 const int64_t col0 = (int64_t)nt * 256 + wg * 128, row0 = m0 + rank * 128 + quarter * 32;
@@ -360,16 +364,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                     const int64_t col = col0 + 32 * c;
                     if (lane == 0 && row0 < p.g.nb && col < p.g.out_dim) tma_store_2d(&p.tmap_y, box, (int)col, (int)row0);
                 }
-            } else if (row < p.g.nb) {
-                const int64_t col0 = (int64_t)nt * 256 + wg * 128;
+            } else {
+                // rows that no tensor store can reach: 16 columns at a time through the box, so that
+                // half a warp writes neighbouring elements of a row
+                const int64_t col0 = (int64_t)nt * 256 + wg * 128 + (lane & 15), row0 = m0 + rank * 128 + quarter * 32;
 #pragma unroll
-                for (int c = 0; c < 128; ++c) {
-                    const float f = c & 1 ? acc[c / 2].y : acc[c / 2].x;
-                    if (col0 + c < p.g.out_dim) {
-                        const int64_t at = row * p.g.out_dim + col0 + c;
-                        if (p.g.y_type == Q4A_F32) static_cast<float*>(p.g.y)[at] = f;
-                        else if (p.g.y_type == Q4A_F16) static_cast<__half*>(p.g.y)[at] = __float2half_rn(f);
-                        else static_cast<__nv_bfloat16*>(p.g.y)[at] = __float2bfloat16_rn(f);
+                for (int c = 0; c < 8; ++c) {
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        sts_f32(box + (uint32_t)(lane * 17 + 2 * k) * 4u, acc[8 * c + k].x);
+                        sts_f32(box + (uint32_t)(lane * 17 + 2 * k + 1) * 4u, acc[8 * c + k].y);
+                    }
+                    __syncwarp();
+#pragma unroll 4
+                    for (int r = lane >> 4; r < 32; r += 2) {
+                        float f;
+                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(box + (uint32_t)(r * 17 + (lane & 15)) * 4u));
+                        if (row0 + r < p.g.nb && col0 + 16 * c < p.g.out_dim) {
+                            const int64_t at = (row0 + r) * p.g.out_dim + col0 + 16 * c;
+                            if (p.g.y_type == Q4A_F32) static_cast<float*>(p.g.y)[at] = f;
+                            else if (p.g.y_type == Q4A_F16) static_cast<__half*>(p.g.y)[at] = __float2half_rn(f);
+                            else static_cast<__nv_bfloat16*>(p.g.y)[at] = __float2bfloat16_rn(f);
+                        }
                     }
                 }
             }
@@ -393,6 +410,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
 
 }  // namespace
 
+// y through tensor stores: 16-byte rows, and a tensor that holds a box.
+bool fp8_wide_tma_y(const Fp8Gemm& g) {
+    const int64_t row = g.out_dim * fp8_type_bytes(g.y_type);
+    return row % 16 == 0 && reinterpret_cast<uintptr_t>(g.y) % 16 == 0 && g.nb >= 32 && row >= 128;
+}
+
 q4a_status launch_gemm_fp8_wide(const Fp8Gemm& g, cudaStream_t stream) {
     int dev = 0, sms = 0;
     q4a_status st = fp8_sm_count(&dev, &sms);
@@ -414,9 +437,8 @@ q4a_status launch_gemm_fp8_wide(const Fp8Gemm& g, cudaStream_t stream) {
     p.n_tiles = (int32_t)n_tiles;
     p.xs_vec = p.nk % 4 == 0 && reinterpret_cast<uintptr_t>(g.x_scale) % 16 == 0;
     const int64_t size = fp8_type_bytes(g.y_type);
-    // y through tensor stores: 16-byte rows, and a tensor that holds a box
-    if (!gated_form && g.out_dim * size % 16 == 0 && reinterpret_cast<uintptr_t>(g.y) % 16 == 0 && g.nb >= 32 &&
-        g.out_dim * size >= 128) {
+    const bool tma_y = !gated_form && fp8_wide_tma_y(g);
+    if (tma_y) {
         const cuuint64_t dims[2] = {(cuuint64_t)g.out_dim, (cuuint64_t)g.nb};
         const cuuint64_t strides[1] = {(cuuint64_t)(g.out_dim * size)};
         const cuuint32_t box[2] = {(cuuint32_t)(128 / size), 32u};
@@ -428,9 +450,8 @@ q4a_status launch_gemm_fp8_wide(const Fp8Gemm& g, cudaStream_t stream) {
                                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
         if (r != CUDA_SUCCESS) return cuda_fail_drv(r);
-        p.y_tma = 1;
     }
-    auto kernel = gated_form ? wide_kernel<true> : wide_kernel<false>;
+    auto kernel = gated_form ? wide_kernel<true, false> : tma_y ? wide_kernel<false, true> : wide_kernel<false, false>;
     st = fp8_allow_smem(kernel, dev, kWdSmem);
     if (st != Q4A_OK) return st;
     const int64_t tiles = m_tiles * n_tiles, pairs = sms / 2;

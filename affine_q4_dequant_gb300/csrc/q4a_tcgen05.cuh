@@ -24,6 +24,18 @@ __device__ __forceinline__ void tc_dealloc(uint32_t taddr, uint32_t cols) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
 }
 
+// The same with a constant column count.
+template <int COLS>
+__device__ __forceinline__ void tc_alloc_n(uint32_t slot_smem) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot_smem), "n"(COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+template <int COLS>
+__device__ __forceinline__ void tc_dealloc_n(uint32_t taddr) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(COLS) : "memory");
+}
+
 // Shared-memory matrix descriptor: K-major operand of 128-byte rows, 128-byte swizzle,
 // 8-row groups 1024 bytes apart, descriptor version 1.
 __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr) {
