@@ -84,8 +84,16 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
 }
 
-// A block's scale from its largest magnitude (fmaxf drops a NaN, so the scale is the other values').
-__device__ __forceinline__ float fp8_scale(float amax) { return fmaxf(amax, kFp8Floor) / kFp8Top; }
+// A block's scale from its largest magnitude (fmaxf drops a NaN, so the scale is the other values'):
+// a product with the rounded 1 / 448, within a unit in the last place of the quotient.
+__device__ __forceinline__ float fp8_scale(float amax) { return fmaxf(amax, kFp8Floor) * (1.0f / kFp8Top); }
+// 1 / scale by the approximate reciprocal, one unit in the last place (scale is a normal number or
+// infinite): the codes that it leads to have 3 mantissa bits.
+__device__ __forceinline__ float fp8_inverse(float scale) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(scale));
+    return r;
+}
 
 // silu(g) * u with the fast exponential and quotient (2 + 1.2 |g| and 2 units in the last place):
 // the result is rounded to 3 mantissa bits, and the exact forms cost the gated epilogue twice the

@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kNwThreads, Narrow<N, T>::R) narrow_kernel(con
                 float amax = fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w)));
 #pragma unroll
                 for (int s = 16; s > 0; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
-                const float scale = fp8_scale(amax), inv = 1.f / scale;
+                const float scale = fp8_scale(amax), inv = fp8_inverse(scale);
                 *reinterpret_cast<uint32_t*>(p.g.q + row * p.g.out_dim + o) =
                     e4m3x4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
                 if (lane == 0) p.g.scale[row * (p.g.out_dim / kFp8Block) + o0 / kFp8Block] = scale;

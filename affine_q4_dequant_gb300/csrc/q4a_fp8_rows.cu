@@ -78,26 +78,27 @@ __device__ __forceinline__ void store16(T* p, float (&v)[kRowElems], bool write)
     }
 }
 
-// Rows to 8 bits. `wpr` warps share a row, thread t of them holding elements 16 t .. 16 t + 15 of
-// each of NC chunks in registers, so the row is read once: the sum of squares, the blocks' maxima
-// (8 threads a block) and the codes all come from those registers.
+// Rows to 8 bits. blockDim.x threads share a row, blockDim.y rows a CTA: `wpr` warps, or with
+// wpr == 1 a power of two of lanes (short rows share a warp). Thread t of them holds elements 16 t ..
+// 16 t + 15 of each of NC chunks in registers, so the row is read once: the sum of squares, the
+// blocks' maxima (8 threads a block) and the codes all come from those registers. Bound by HBM:
+// 8192 x 4096 with a residual takes 35.9 us in bf16 (6.5 TB/s) and 69.4 us in fp32 (6.3 TB/s).
 template <typename XT, typename RT, bool RES, bool NORM, int NC>
 __global__ void __launch_bounds__(NC == 1 ? 1024 : 512)
     fp8_rows_kernel(const Fp8Norm p, int wpr) {
     __shared__ float s_red[32];
     grid_dep_wait();
     grid_dep_launch();
-    const int warp = threadIdx.x >> 5;
-    const int rpc = (blockDim.x >> 5) / wpr;                 // rows of this CTA
-    const int64_t row = (int64_t)blockIdx.x * rpc + warp / wpr;
-    const int t = (int)threadIdx.x - warp / wpr * wpr * 32;  // thread within the row
+    const int tpr = blockDim.x;                              // threads of a row
+    const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const int t = threadIdx.x;
     const bool live = row < p.nb;
     const int64_t nblk = (p.dim + kFp8Block - 1) / kFp8Block;
     float v[NC][kRowElems];
     float ssq = 0.f;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-        const int64_t e = ((int64_t)c * wpr * 32 + t) * kRowElems;
+        const int64_t e = ((int64_t)c * tpr + t) * kRowElems;
         const bool on = live && e < p.dim;
 #pragma unroll
         for (int i = 0; i < kRowElems; ++i) v[c][i] = 0.f;
@@ -118,12 +119,11 @@ __global__ void __launch_bounds__(NC == 1 ? 1024 : 512)
     }
     float rstd = 1.f;
     if (NORM) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ssq += __shfl_xor_sync(0xffffffffu, ssq, o);
+        for (int o = wpr > 1 ? 16 : tpr >> 1; o > 0; o >>= 1) ssq += __shfl_xor_sync(0xffffffffu, ssq, o);
         if (wpr > 1) {
-            if ((threadIdx.x & 31) == 0) s_red[warp] = ssq;
+            const int w0 = (int)threadIdx.y * wpr;
+            if ((t & 31) == 0) s_red[w0 + (t >> 5)] = ssq;
             __syncthreads();
-            const int w0 = warp / wpr * wpr;
             ssq = 0.f;
             for (int w = 0; w < wpr; ++w) ssq += s_red[w0 + w];
         }
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(NC == 1 ? 1024 : 512)
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-        const int64_t e = ((int64_t)c * wpr * 32 + t) * kRowElems;
+        const int64_t e = ((int64_t)c * tpr + t) * kRowElems;
         const bool on = live && e < p.dim;
         if (NORM && on) {
             float w[kRowElems];
@@ -143,10 +143,11 @@ __global__ void __launch_bounds__(NC == 1 ? 1024 : 512)
 #pragma unroll
         for (int i = 0; i < kRowElems; ++i) amax = fmaxf(amax, fabsf(v[c][i]));
 #pragma unroll
-        for (int o = 1; o < kFp8Block / kRowElems; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        for (int o = 1; o < kFp8Block / kRowElems; o <<= 1)   // (fewer threads: a row is within one block)
+            if (o < tpr) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         if (on) {
             const float scale = fp8_scale(amax);
-            const float inv = 1.f / scale;
+            const float inv = fp8_inverse(scale);
             uint32_t o[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -157,19 +158,125 @@ __global__ void __launch_bounds__(NC == 1 ? 1024 : 512)
     }
 }
 
+// Activations whose rows are whole blocks: one run of n elements, 16 a thread and step, with neither
+// rows nor barriers, so that many small CTAs keep loads and stores in flight together
+// (4096 x 12288 bf16: 23.0 us, 6.6 TB/s; by rows of 768 threads 29.3 us).
+__device__ __forceinline__ float amax16(const uint4 (&w)[4], const float*) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        m = fmaxf(fmaxf(fmaxf(m, fabsf(__uint_as_float(w[i].x))), fabsf(__uint_as_float(w[i].y))),
+                  fmaxf(fabsf(__uint_as_float(w[i].z)), fabsf(__uint_as_float(w[i].w))));
+    return m;
+}
+__device__ __forceinline__ float2 pair_max(uint32_t (&w)[8], const __half* t) {
+    __half2 m = __float2half2_rn(0.f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<__half2*>(&w[i])));
+    return __half22float2(m);
+}
+__device__ __forceinline__ float2 pair_max(uint32_t (&w)[8], const __nv_bfloat16* t) {
+    __nv_bfloat162 m = __float2bfloat162_rn(0.f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<__nv_bfloat162*>(&w[i])));
+    return __bfloat1622float2(m);
+}
+// Largest magnitudes in pairs, in the type itself: exact, and half the conversions and comparisons.
+template <typename T>
+__device__ __forceinline__ float amax16(const uint4 (&w)[2], const T* t) {
+    uint32_t p[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+    const float2 m = pair_max(p, t);
+    return fmaxf(m.x, m.y);
+}
+__device__ __forceinline__ void values16(const uint4 (&w)[4], float (&v)[kRowElems], const float*) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[4 * i] = __uint_as_float(w[i].x);
+        v[4 * i + 1] = __uint_as_float(w[i].y);
+        v[4 * i + 2] = __uint_as_float(w[i].z);
+        v[4 * i + 3] = __uint_as_float(w[i].w);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void values16(const uint4 (&w)[2], float (&v)[kRowElems], const T* t) {
+    const uint32_t p[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 f = pair_f32(p[i], t);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+
+constexpr int kFlatThreads = 256, kFlatSteps = 2;
+
+template <typename XT>
+__global__ void __launch_bounds__(kFlatThreads)
+    fp8_flat_kernel(uint8_t* __restrict__ q, float* __restrict__ scale, const XT* __restrict__ x, int64_t chunks) {
+    constexpr int V = kRowElems * (int)sizeof(XT) / 16;   // 16-byte vectors of a chunk
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t c0 = (int64_t)blockIdx.x * (kFlatThreads * kFlatSteps) + threadIdx.x;
+    uint4 w[kFlatSteps][V];
+#pragma unroll
+    for (int s = 0; s < kFlatSteps; ++s) {
+        const int64_t c = c0 + s * kFlatThreads;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            w[s][i] = c < chunks ? ld_nc_16(reinterpret_cast<const uint4*>(x) + c * V + i) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int s = 0; s < kFlatSteps; ++s) {
+        const int64_t c = c0 + s * kFlatThreads;
+        float amax = amax16(w[s], x);
+#pragma unroll
+        for (int o = 1; o < kFp8Block / kRowElems; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const float sc = fp8_scale(amax), inv = fp8_inverse(sc);
+        float v[kRowElems];
+        values16(w[s], v, x);
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = e4m3x4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+        if (c < chunks) {
+            reinterpret_cast<uint4*>(q)[c] = make_uint4(o[0], o[1], o[2], o[3]);
+            if ((c & (kFp8Block / kRowElems - 1)) == 0) scale[c / (kFp8Block / kRowElems)] = sc;
+        }
+    }
+}
+
+template <typename XT>
+q4a_status launch_flat(const Fp8Norm& n, cudaStream_t stream) {
+    const int64_t chunks = n.nb * (n.dim / kRowElems);
+    const int64_t ctas = (chunks + kFlatThreads * kFlatSteps - 1) / (kFlatThreads * kFlatSteps);
+    if (ctas > ((int64_t)1 << 31) - 1) return Q4A_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+    cfg.blockDim = dim3(kFlatThreads, 1, 1);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_flat_kernel<XT>, n.q, n.scale, static_cast<const XT*>(n.x), chunks);
+    return e == cudaSuccess ? Q4A_OK : cuda_fail(e);
+}
+
 template <typename XT, typename RT, bool RES, bool NORM>
 q4a_status launch_rows_typed(const Fp8Norm& n, cudaStream_t stream) {
     // one chunk per thread up to 1024 threads (16384 columns), else four
     const bool wide = n.dim > 1024 * kRowElems;
     const int64_t threads = (n.dim + kRowElems - 1) / kRowElems;
     const int wpr = (int)((wide ? (threads + 127) / 128 : (threads + 31) / 32));
-    const int rpc = wpr >= 8 ? 1 : 8 / wpr;
+    int lpr = 32;
+    while (wpr == 1 && lpr / 2 >= threads) lpr /= 2;
+    const int rpc = wpr > 1 ? (wpr >= 8 ? 1 : 8 / wpr) : 256 / lpr;   // rows of a CTA
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3((unsigned)((n.nb + rpc - 1) / rpc), 1, 1);
-    cfg.blockDim = dim3((unsigned)(32 * wpr * rpc), 1, 1);
+    cfg.blockDim = dim3((unsigned)(wpr > 1 ? 32 * wpr : lpr), (unsigned)rpc, 1);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -180,7 +287,8 @@ q4a_status launch_rows_typed(const Fp8Norm& n, cudaStream_t stream) {
 
 template <typename XT>
 q4a_status launch_rows_x(const Fp8Norm& n, cudaStream_t stream) {
-    if (!n.norm_w) return launch_rows_typed<XT, float, false, false>(n, stream);
+    if (!n.norm_w)
+        return n.dim % kFp8Block == 0 ? launch_flat<XT>(n, stream) : launch_rows_typed<XT, float, false, false>(n, stream);
     if (!n.residual) return launch_rows_typed<XT, float, false, true>(n, stream);
     if (n.res_type == Q4A_F32) return launch_rows_typed<XT, float, true, true>(n, stream);
     if (n.res_type == Q4A_F16) return launch_rows_typed<XT, __half, true, true>(n, stream);
@@ -188,39 +296,35 @@ q4a_status launch_rows_x(const Fp8Norm& n, cudaStream_t stream) {
 }
 
 // Packed 4-bit weights to 8-bit blocks. A CTA takes 128 rows x 256 columns (two blocks); a warp 16
-// rows, 4 at a time, 8 lanes a row; a lane 32 codes (16 bytes), half of a 64-input group.
+// rows, 8 at a time, 4 lanes a row; a lane a 64-input group (32 bytes of codes).
 //
-// Reading 0.56 and writing 1 byte a weight leaves an SM's 128 lanes about 8 instructions a weight at
-// the HBM rate, so neither pass works on single weights. W is monotonic in the code (so is the
-// rounded multiply-add): a group's largest magnitude is at its smallest or largest code, found on
-// pairs of codes where they lie in the packed word. And a group has 16 possible results: its two
-// lanes round 8 each to e4m3, and a code becomes its byte by permutes over that table.
+// Reading 0.56 and writing 1 byte a weight leaves an SM's 64 integer lanes about 4 instructions a
+// weight at the HBM rate, so neither pass works on single weights. W is monotonic in the code (so is
+// the rounded multiply-add): a group's largest magnitude is at its smallest or largest code, found on
+// pairs of codes where they lie in the packed word. And a group has 16 possible results: the lane
+// rounds those to e4m3, and a code becomes its byte by permutes over that table. 151936 x 4096 takes
+// 172 us (5.7 TB/s); with both passes on single weights it took 322 us.
 constexpr int kDqCols = 256;
 
-__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("min.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-// Smallest and largest code of four packed words.
-__device__ __forceinline__ void code_range(const uint4& q, uint32_t& lo, uint32_t& hi) {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    uint32_t h[4], l[4];
+// Smallest and largest code of eight packed words. Field f of a word's halves is compared in place:
+// the fields below it may stay, the ones above it are masked off.
+__device__ __forceinline__ void code_range(const uint32_t (&w)[8], uint32_t& lo, uint32_t& hi) {
+    uint32_t h = 0u, l = 0x000F000Fu;
 #pragma unroll
-    for (int f = 0; f < 4; ++f) {   // field f of both halves of every word, in place
-        const uint32_t m = 0x000F000Fu << (4 * f);
-        h[f] = max2(max2(w[0] & m, w[1] & m), max2(w[2] & m, w[3] & m)) >> (4 * f);
-        l[f] = min2(min2(w[0] & m, w[1] & m), min2(w[2] & m, w[3] & m)) >> (4 * f);
+    for (int f = 3; f >= 0; --f) {
+        const uint32_t m = 0xFFFFu >> (4 * (3 - f)), mm = m | m << 16;
+        uint32_t v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = w[i] & mm;
+        const uint32_t a = __vimax3_u16x2(__vimax3_u16x2(v[0], v[1], v[2]), __vimax3_u16x2(v[3], v[4], v[5]),
+                                          __vmaxu2(v[6], v[7]));
+        const uint32_t b = __vimin3_u16x2(__vimin3_u16x2(v[0], v[1], v[2]), __vimin3_u16x2(v[3], v[4], v[5]),
+                                          __vminu2(v[6], v[7]));
+        h = __vmaxu2(h, (a >> (4 * f)) & 0x000F000Fu);
+        l = __vminu2(l, (b >> (4 * f)) & 0x000F000Fu);
     }
-    const uint32_t a = max2(max2(h[0], h[1]), max2(h[2], h[3])), b = min2(min2(l[0], l[1]), min2(l[2], l[3]));
-    hi = max(a & 0xFFFFu, a >> 16);
-    lo = min(b & 0xFFFFu, b >> 16);
+    hi = max(h & 0xFFFFu, h >> 16);
+    lo = min(l & 0xFFFFu, l >> 16);
 }
 
 // The bytes of codes 0..3 of a packed half word, from the tables of codes 0..7 (t0, t1) and 8..15
@@ -241,65 +345,65 @@ __global__ void __launch_bounds__(256)
     const int64_t groups = in_dim / kGroup, nblk = (in_dim + kFp8Block - 1) / kFp8Block;
     const int64_t tiles = (in_dim + kDqCols - 1) / kDqCols;
     const int64_t rb = blockIdx.x / tiles, ct = blockIdx.x - rb * tiles;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = lane & 7;
-    const int64_t col = ct * kDqCols + part * 32, row0 = rb * kFp8Block + warp * 16 + (lane >> 3);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = lane & 3;
+    const int64_t col = ct * kDqCols + part * kGroup, row0 = rb * kFp8Block + warp * 16 + (lane >> 2);
     const bool col_on = col < in_dim;
-    uint4 q[4];
-    uint16_t sb[4], bb[4];
+    uint32_t q[2][8];
+    float sv[2], bv[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t row = row0 + 4 * i;
+    for (int i = 0; i < 2; ++i) {
+        const int64_t row = row0 + 8 * i;
         const bool on = col_on && row < rows;
-        q[i] = on ? ld_nc_16(w + row * (in_dim / 2) + col / 2) : make_uint4(0, 0, 0, 0);
-        sb[i] = on ? __ldg(s + row * groups + col / kGroup) : (uint16_t)0;
-        bb[i] = on ? __ldg(b + row * groups + col / kGroup) : (uint16_t)0;
+        const uint8_t* src = w + row * (in_dim / 2) + col / 2;
+        const uint4 a = on ? ld_nc_16(src) : make_uint4(0, 0, 0, 0), c = on ? ld_nc_16(src + 16) : make_uint4(0, 0, 0, 0);
+        q[i][0] = a.x, q[i][1] = a.y, q[i][2] = a.z, q[i][3] = a.w;
+        q[i][4] = c.x, q[i][5] = c.y, q[i][6] = c.z, q[i][7] = c.w;
+        sv[i] = on ? bf16_to_f32(__ldg(s + row * groups + col / kGroup)) : 0.f;
+        bv[i] = on ? bf16_to_f32(__ldg(b + row * groups + col / kGroup)) : 0.f;
     }
     float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
         uint32_t lo, hi;
         code_range(q[i], lo, hi);
-        const float sv = bf16_to_f32(sb[i]), bv = bf16_to_f32(bb[i]);
-        amax = fmaxf(amax, fmaxf(fabsf(fmaf(sv, (float)lo, bv)), fabsf(fmaf(sv, (float)hi, bv))));
+        amax = fmaxf(amax, fmaxf(fabsf(fmaf(sv[i], (float)lo, bv[i])), fabsf(fmaf(sv[i], (float)hi, bv[i]))));
     }
-    // lanes of a block: 4 of a row's 8, in all 4 rows
+    // lanes of a block: 2 of a row's 4, in all 8 rows
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 8));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     if (lane == 0) s_max[0][warp] = amax;
-    if (lane == 4) s_max[1][warp] = amax;
+    if (lane == 2) s_max[1][warp] = amax;
     __syncthreads();
-    const int blk = part >> 2;
+    const int blk = part >> 1;
     amax = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) amax = fmaxf(amax, s_max[blk][i]);
-    const float scale = fp8_scale(amax), inv = 1.f / scale;
-    if (warp == 0 && (lane == 0 || lane == 4) && col_on) w_scale[rb * nblk + 2 * ct + blk] = scale;
-    const float first = (float)((lane & 1) * 8);   // this lane's half of the group's table
+    const float scale = fp8_scale(amax), inv = fp8_inverse(scale);
+    if (warp == 0 && (lane == 0 || lane == 2) && col_on) w_scale[rb * nblk + 2 * ct + blk] = scale;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float sv = bf16_to_f32(sb[i]), bv = bf16_to_f32(bb[i]);
-        float v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = fmaf(sv, first + (float)k, bv) * inv;
-        const uint32_t m0 = e4m3x4(v[0], v[1], v[2], v[3]), m1 = e4m3x4(v[4], v[5], v[6], v[7]);
-        const uint32_t o0 = __shfl_xor_sync(0xffffffffu, m0, 1), o1 = __shfl_xor_sync(0xffffffffu, m1, 1);
-        const bool odd = lane & 1;
-        const uint32_t t0 = odd ? o0 : m0, t1 = odd ? o1 : m1, t2 = odd ? m0 : o0, t3 = odd ? m1 : o1;
-        const uint32_t word[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-        uint32_t out[8];
+    for (int i = 0; i < 2; ++i) {
+        uint32_t t[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const uint32_t low3 = word[k] & 0x77777777u, bit3 = (word[k] >> 3) & 0x11111111u;
-            out[2 * k] = table_bytes(low3, bit3, t0, t1, t2, t3);
-            out[2 * k + 1] = table_bytes(low3 >> 16, bit3 >> 16, t0, t1, t2, t3);
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = fmaf(sv[i], (float)(4 * k + e), bv[i]) * inv;
+            t[k] = e4m3x4(v[0], v[1], v[2], v[3]);
         }
-        const int64_t row = row0 + 4 * i;
-        if (col_on && row < rows) {
-            uint4* dst = reinterpret_cast<uint4*>(w8 + row * in_dim + col);
-            dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-            dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+        const int64_t row = row0 + 8 * i;
+        const bool on = col_on && row < rows;
+        uint4* dst = reinterpret_cast<uint4*>(w8 + row * in_dim + col);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t out[4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t word = q[i][2 * k + h], low3 = word & 0x77777777u, bit3 = (word >> 3) & 0x11111111u;
+                out[2 * h] = table_bytes(low3, bit3, t[0], t[1], t[2], t[3]);
+                out[2 * h + 1] = table_bytes(low3 >> 16, bit3 >> 16, t[0], t[1], t[2], t[3]);
+            }
+            if (on) dst[k] = make_uint4(out[0], out[1], out[2], out[3]);
         }
     }
 }

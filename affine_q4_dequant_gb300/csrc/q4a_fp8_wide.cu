@@ -39,7 +39,7 @@ constexpr int kWdS = 5;                            // stages
 // added.
 constexpr int kWdSL = kWdS + 2;
 constexpr int kWdSlot = (128 + 2) * 16;
-constexpr int kWdBox = 32 * 128;                   // y store box of a warp: 32 rows of 128 bytes
+constexpr int kWdBox = 2 * 32 * 64;                // a warp's two y store boxes: 32 rows of 64 bytes
 constexpr int kWdScales = kWdS * kWdStage;
 constexpr int kWdY = (kWdScales + kWdSL * kWdSlot + 1023) / 1024 * 1024;
 constexpr int kWdMax = kWdY + kWdAddWarps * kWdBox;              // gated: rows' maxima, [2][128]
@@ -52,7 +52,7 @@ static_assert(kWdSmem <= 227 * 1024, "shared memory");
 struct WideParams {
     CUtensorMap tmap_w;    // e4m3 [weight rows][in_dim], box 128 bytes x 128 rows, 128-byte swizzle
     CUtensorMap tmap_x;    // e4m3 [nb][in_dim], the same box
-    CUtensorMap tmap_y;    // y [nb][out_dim], box 128 bytes x 32 rows, 128-byte swizzle (kernels with TMA_Y)
+    CUtensorMap tmap_y;    // y [nb][out_dim], box 64 bytes x 32 rows, 64-byte swizzle (kWdF32, kWdF16, kWdBf16)
     Fp8Gemm g;
     int32_t nk;            // column blocks
     int32_t m_tiles, n_tiles;
@@ -126,8 +126,13 @@ __device__ __forceinline__ void tile_at(const WideParams& p, int t, int64_t& m0,
     nt = in / rows;
 }
 
-__device__ __forceinline__ uint32_t pack_y(float a, float b, int type) {
-    if (type == Q4A_F16) {
+// How the tile leaves: the gated form's 8-bit rows; y through shared memory and tensor stores, by its
+// type; or y element by element.
+enum WideOut : int { kWdGated, kWdF32, kWdF16, kWdBf16, kWdScalar };
+
+template <WideOut OUT>
+__device__ __forceinline__ uint32_t pack_y(float a, float b) {
+    if (OUT == kWdF16) {
         const __half2 h = __floats2half2_rn(a, b);
         return *reinterpret_cast<const uint32_t*>(&h);
     }
@@ -135,10 +140,10 @@ __device__ __forceinline__ uint32_t pack_y(float a, float b, int type) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// TMA_Y: y leaves through shared memory and tensor stores.
-template <bool GATED, bool TMA_Y>
+template <WideOut OUT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
     wide_kernel(const __grid_constant__ WideParams p) {
+    constexpr bool GATED = OUT == kWdGated;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -262,10 +267,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
         uint32_t sl_phase = 1;
         float2 acc[64];
         for (int t = pair; t < tiles; t += pairs) {
-            int64_t m0;
-            int nt;
-            tile_at(p, t, m0, nt);
-            const int64_t row = m0 + rank * 128 + rl;
 #pragma unroll
             for (int c = 0; c < 64; ++c) acc[c] = make_float2(0.f, 0.f);
             for (int kb = 0; kb < nk; ++kb, ++i) {
@@ -302,7 +303,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                     if (c < 7) tc_ld16_wait(d[(c + 1) & 1]);
                 }
             }
+            int64_t m0;
+            int nt;
+            tile_at(p, t, m0, nt);
             if (GATED) {
+                const int64_t row = m0 + rank * 128 + rl;
                 float amax = 0.f;
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
@@ -316,7 +321,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                 asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
                 amax = fmaxf(amax, s_max[(1 - wg) * 128 + rl]);
                 asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
-                const float scale = fp8_scale(amax), inv = 1.f / scale;
+                const float scale = fp8_scale(amax), inv = fp8_inverse(scale);
                 if (row < p.g.nb) {
                     uint4* q = reinterpret_cast<uint4*>(p.g.q + row * p.g.out_dim + (int64_t)nt * 128 + wg * 64);
 #pragma unroll
@@ -331,38 +336,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                     }
                     if (wg == 0) p.g.scale[row * (p.g.out_dim / kFp8Block) + nt] = scale;
                 }
-            } else if (TMA_Y) {
-                // 128 bytes of a row at a time through this warp's box (16-byte unit u of row r at
-                // u ^ (r & 7)), rows and columns beyond y clipped by the tensor map
+            } else if (OUT != kWdScalar) {
+                // 64 bytes of a row at a time through one of this warp's two boxes (16-byte unit u of row
+                // r at u ^ (r / 2 & 3)), rows and columns beyond y clipped by the tensor map
                 const int64_t col0 = (int64_t)nt * 256 + wg * 128, row0 = m0 + rank * 128 + quarter * 32;
-                const bool f32 = p.g.y_type == Q4A_F32;
-                const uint32_t line = box + (uint32_t)lane * 128u, sw = (uint32_t)lane & 7u;
+                constexpr bool f32 = OUT == kWdF32;
+                const uint32_t line = (uint32_t)lane * 64u, sw = ((uint32_t)lane >> 1) & 3u;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 8; ++c) {       // 16 columns of 4 bytes, or 32 of 2
                     if (!f32 && (c & 1)) continue;
-                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    const uint32_t half = box + (uint32_t)((f32 ? c : c / 2) & 1) * (kWdBox / 2);
+                    if (lane == 0) bulk_wait_read_1();
                     __syncwarp();
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        uint32_t v[4];
-                        if (f32) {
-                            const float2 a = acc[16 * c + 2 * u], b = acc[16 * c + 2 * u + 1];
-                            v[0] = __float_as_uint(a.x), v[1] = __float_as_uint(a.y), v[2] = __float_as_uint(b.x), v[3] = __float_as_uint(b.y);
+                    for (int u = 0; u < 4; ++u) {
+                        const uint32_t at = half + line + (((uint32_t)u ^ sw) << 4);
+                        if (f32) {   // in pairs, as the multiply-adds hold them: quads cost spills
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+                                asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(at + 8u * k), "f"(acc[8 * c + 2 * u + k].x),
+                                             "f"(acc[8 * c + 2 * u + k].y)
+                                             : "memory");
                         } else {
+                            uint32_t v[4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                const float2 a = acc[(16 * c + 4 * u + k) & 63];
-                                v[k] = pack_y(a.x, a.y, p.g.y_type);
+                                const float2 a = acc[(8 * c + 4 * u + k) & 63];
+                                v[k] = pack_y<OUT>(a.x, a.y);
                             }
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                                         "r"(v[3])
+                                         : "memory");
                         }
-                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(line + (((uint32_t)u ^ sw) << 4)), "r"(v[0]),
-                                     "r"(v[1]), "r"(v[2]), "r"(v[3])
-                                     : "memory");
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
-                    const int64_t col = col0 + 32 * c;
-                    if (lane == 0 && row0 < p.g.nb && col < p.g.out_dim) tma_store_2d(&p.tmap_y, box, (int)col, (int)row0);
+                    const int64_t col = col0 + 16 * c;
+                    if (lane == 0 && row0 < p.g.nb && col < p.g.out_dim) tma_store_2d(&p.tmap_y, half, (int)col, (int)row0);
                 }
             } else {
                 // rows that no tensor store can reach: 16 columns at a time through the box, so that
@@ -413,7 +423,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
 // y through tensor stores: 16-byte rows, and a tensor that holds a box.
 bool fp8_wide_tma_y(const Fp8Gemm& g) {
     const int64_t row = g.out_dim * fp8_type_bytes(g.y_type);
-    return row % 16 == 0 && reinterpret_cast<uintptr_t>(g.y) % 16 == 0 && g.nb >= 32 && row >= 128;
+    return row % 16 == 0 && reinterpret_cast<uintptr_t>(g.y) % 16 == 0 && g.nb >= 32 && row >= 64;
 }
 
 q4a_status launch_gemm_fp8_wide(const Fp8Gemm& g, cudaStream_t stream) {
@@ -441,17 +451,20 @@ q4a_status launch_gemm_fp8_wide(const Fp8Gemm& g, cudaStream_t stream) {
     if (tma_y) {
         const cuuint64_t dims[2] = {(cuuint64_t)g.out_dim, (cuuint64_t)g.nb};
         const cuuint64_t strides[1] = {(cuuint64_t)(g.out_dim * size)};
-        const cuuint32_t box[2] = {(cuuint32_t)(128 / size), 32u};
+        const cuuint32_t box[2] = {(cuuint32_t)(64 / size), 32u};
         const cuuint32_t estr[2] = {1u, 1u};
         const CUtensorMapDataType dt = g.y_type == Q4A_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                        : g.y_type == Q4A_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                              : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
         r = encode_tiled_cached(&p.tmap_y, dt, 2, g.y, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                                CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
         if (r != CUDA_SUCCESS) return cuda_fail_drv(r);
     }
-    auto kernel = gated_form ? wide_kernel<true, false> : tma_y ? wide_kernel<false, true> : wide_kernel<false, false>;
+    auto kernel = gated_form ? wide_kernel<kWdGated>
+                  : !tma_y ? wide_kernel<kWdScalar>
+                  : g.y_type == Q4A_F32 ? wide_kernel<kWdF32>
+                  : g.y_type == Q4A_F16 ? wide_kernel<kWdF16> : wide_kernel<kWdBf16>;
     st = fp8_allow_smem(kernel, dev, kWdSmem);
     if (st != Q4A_OK) return st;
     const int64_t tiles = m_tiles * n_tiles, pairs = sms / 2;

@@ -411,7 +411,7 @@ Q4A_API q4a_status q4a_moe_combine(float* out, const float* y, const int32_t* sl
  *                w_scale [ceil(out_dim/128)][ceil(in_dim/128)]
  *   The value is code * scale. Where this library writes scales, a block of values v gets
  *       scale = max(max|v|, 2^-100) / 448,   code = e4m3(v * (1 / scale)), round to nearest even,
- *   in fp32; a block of zeros has scale 2^-100 / 448 and zero codes. The scales that a product
+ *   in fp32 (the scale and 1 / scale to a unit in the last place); a block of zeros has scale 2^-100 / 448 and zero codes. The scales that a product
  *   reads are any fp32 values. The last block of a row or column may be short. A NaN becomes a
  *   NaN code and leaves its block's scale to the other values; an infinity makes its block's
  *   scale infinite: either comes out of a product as NaN.
