@@ -133,23 +133,23 @@ _F16 = (torch.float16, torch.int16, torch.uint16)
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
-_F8 = (torch.float8_e4m3fn, torch.uint8)
+_E4M3 = torch.float8_e4m3fn
+_F8 = (_E4M3, torch.uint8)
 _TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}   # q4a_type
 _ANY = None   # any dtype (prefetch hints)
-_NULL = ctypes.c_void_p(0)
 
 
 def _ptrs(*specs):
     """Device pointers for specs (tensor, name, dtypes, shape); a spec may be None (a NULL
-    pointer). A mis-shaped buffer would be read or written past its end by the kernels, so it is
+    pointer) or the address of a buffer that the binding has just allocated. A mis-shaped buffer would be read or written past its end by the kernels, so it is
     refused here, before anything launches. This runs on every call: one pass over plain
     comparisons and C-level tensor queries, and _refuse finds what to say where one fails."""
     out = []
     try:
         dev = _cuda_device()
         for sp in specs:
-            if sp is None:
-                out.append(_NULL)
+            if sp is None or sp.__class__ is int:
+                out.append(sp)
                 continue
             t, _, dtypes, shape = sp
             if (shape is not None and t.shape != shape) or (dtypes is not None and t.dtype not in dtypes) \
@@ -167,7 +167,7 @@ def _refuse(*specs):
     """Raises for the first wrong spec: every shape is checked first, then dtypes, CUDA residency,
     the device and contiguity. Returns the pointers if nothing is wrong."""
     for sp in specs:
-        if sp is None:
+        if sp is None or sp.__class__ is int:
             continue
         t, name, _, shape = sp
         if not isinstance(t, torch.Tensor):
@@ -177,8 +177,8 @@ def _refuse(*specs):
     dev = None
     out = []
     for sp in specs:
-        if sp is None:
-            out.append(_NULL)
+        if sp is None or sp.__class__ is int:
+            out.append(sp)
             continue
         t, name, dtypes, _ = sp
         if dtypes is not None and t.dtype not in dtypes:
@@ -508,28 +508,25 @@ def moe_combine(y: torch.Tensor, slot: torch.Tensor, w: torch.Tensor, y_shared: 
 
 def _type(t, name: str) -> int:
     """The q4a_type of a tensor (or dtype) that an 8-bit entry point takes in more than one type."""
-    dtype = t.dtype if isinstance(t, torch.Tensor) else t
-    if dtype not in _TYPES:
+    dtype = t if t.__class__ is torch.dtype else t.dtype
+    code = _TYPES.get(dtype)
+    if code is None:
         raise TypeError(f"{name}: dtype {dtype} not in {tuple(_TYPES)}")
-    return _TYPES[dtype]
+    return code
 
 
-def _empty_on(stream, shape, dtype, like):
-    """A buffer from the memory pool of the stream that will use it: a buffer of another stream's
-    pool could be handed on there while this stream's kernels still run."""
+def _out(t, name, dtypes, shape, dtype, like, stream):
+    """An output and its spec: the caller's buffer to be checked, or a new one. A new one comes from
+    the memory pool of the stream that will write it: a buffer of another stream's pool could be
+    handed on there while this stream's kernels still run."""
+    if t is not None:
+        return t, (t, name, dtypes, shape)
     if stream is None:
-        return _empty(shape, dtype, like)
-    with torch.cuda.stream(stream):
-        return _empty(shape, dtype, like)
-
-
-def _fp8_rows(stream, q, scale, nb: int, dim: int, like, qname: str = "q", sname: str = "scale"):
-    """The codes [nb][dim] and scales [nb][ceil(dim/128)] of 8-bit rows, allocated where not given,
-    and their specs."""
-    q = _empty_on(stream, (nb, dim), torch.float8_e4m3fn, like) if q is None else q
-    blocks = (dim + 127) // 128
-    scale = _empty_on(stream, (nb, blocks), torch.float32, like) if scale is None else scale
-    return q, scale, ((q, qname, _F8, (nb, dim)), (scale, sname, _F32, (nb, blocks)))
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    else:
+        with torch.cuda.stream(stream):
+            t = torch.empty(shape, dtype=dtype, device=like.device)
+    return t, t.data_ptr()
 
 
 def _fp8_mat(w, w_scale, out_dim: int, in_dim: int, wname: str = "w", sname: str = "w_scale"):
@@ -543,8 +540,9 @@ def quantize_fp8(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Te
     (q float8_e4m3fn [nb][dim], scale fp32 [nb][ceil(dim/128)])."""
     nb, dim = _dims(x, "x")
     xt = _type(x, "x")
-    q, scale, specs = _fp8_rows(stream, q, scale, nb, dim, x)
-    pq, ps, px = _ptrs(*specs, (x, "x", None, None))
+    q, qs = _out(q, "q", _F8, (nb, dim), _E4M3, x, stream)
+    scale, ss = _out(scale, "scale", _F32, (nb, (dim + 127) // 128), torch.float32, x, stream)
+    pq, ps, px = _ptrs(qs, ss, (x, "x", None, None))
     _check("q4a_quantize_fp8", _lib.q4a_quantize_fp8(pq, ps, px, xt, nb, dim, _stream(stream)))
     return q, scale
 
@@ -557,17 +555,10 @@ def add_rmsnorm_fp8(x, norm_w, residual: torch.Tensor | None = None, eps: float 
     want_x_new is False."""
     nb, dim = _dims(x, "x")
     xt = _type(x, "x")
-    q, scale, specs = _fp8_rows(stream, q, scale, nb, dim, x)
-    rt = 0
-    if residual is not None:
-        rt = _type(residual, "residual")
-        if x_new is None and want_x_new:
-            x_new = _empty_on(stream, (nb, dim), residual.dtype, x)
-    elif x_new is not None:
-        raise ValueError("x_new needs a residual")
-    pq, ps, pn, px, pr, pw = _ptrs(
-        *specs, None if x_new is None else (x_new, "x_new", (residual.dtype,), (nb, dim)), (x, "x", None, None),
-        None if residual is None else (residual, "residual", None, (nb, dim)), (norm_w, "norm_w", _BF16, (dim,)))
+    q, qs = _out(q, "q", _F8, (nb, dim), _E4M3, x, stream)
+    scale, ss = _out(scale, "scale", _F32, (nb, (dim + 127) // 128), torch.float32, x, stream)
+    rt, rs, x_new, ns = _residual(residual, x_new, want_x_new, nb, dim, x, stream)
+    pq, ps, pn, px, pr, pw = _ptrs(qs, ss, ns, (x, "x", None, None), rs, (norm_w, "norm_w", _BF16, (dim,)))
     _check("q4a_add_rmsnorm_fp8", _lib.q4a_add_rmsnorm_fp8(pq, ps, pn, px, xt, pr, rt, pw, float(eps), float(shift),
                                                            nb, dim, _stream(stream)))
     return q, scale, x_new
@@ -578,9 +569,9 @@ def dequant_fp8(w, s, b, out: torch.Tensor | None = None, scale: torch.Tensor | 
     [ceil(rows/128)][ceil(in/128)])."""
     rows, half = _dims(w, "w")
     in_dim = 2 * half
-    out = _empty_on(stream, (rows, in_dim), torch.float8_e4m3fn, w) if out is None else out
-    scale = _empty_on(stream, ((rows + 127) // 128, (in_dim + 127) // 128), torch.float32, w) if scale is None else scale
-    po, pc, pw, ps, pb = _ptrs(*_fp8_mat(out, scale, rows, in_dim, "out", "scale"), *_mat(w, s, b, rows, in_dim))
+    out, os_ = _out(out, "out", _F8, (rows, in_dim), _E4M3, w, stream)
+    scale, cs = _out(scale, "scale", _F32, ((rows + 127) // 128, (in_dim + 127) // 128), torch.float32, w, stream)
+    po, pc, pw, ps, pb = _ptrs(os_, cs, *_mat(w, s, b, rows, in_dim))
     _check("q4a_dequant_fp8", _lib.q4a_dequant_fp8(po, pc, pw, ps, pb, rows, in_dim, _stream(stream)))
     return out, scale
 
@@ -591,9 +582,11 @@ def gemm_fp8(w, w_scale, x, x_scale, out: torch.Tensor | None = None, out_dtype=
     out_dim = _dims(w, "w")[0]
     nb, in_dim = _dims(x, "x")
     yt = _type(out_dtype if out is None else out, "y")
-    out = _empty_on(stream, (nb, out_dim), out_dtype, x) if out is None else out
-    _, _, xs = _fp8_rows(stream, x, x_scale, nb, in_dim, x, "x", "x_scale")
-    py, pw, pws, px, pxs = _ptrs((out, "y", None, (nb, out_dim)), *_fp8_mat(w, w_scale, out_dim, in_dim), *xs)
+    out, ys = _out(out, "y", None, (nb, out_dim), out_dtype, x, stream)
+    blocks = (in_dim + 127) // 128
+    py, pw, pws, px, pxs = _ptrs(ys, (w, "w", _F8, (out_dim, in_dim)),
+                                 (w_scale, "w_scale", _F32, ((out_dim + 127) // 128, blocks)), (x, "x", _F8, None),
+                                 (x_scale, "x_scale", _F32, (nb, blocks)))
     _check("q4a_gemm_fp8", _lib.q4a_gemm_fp8(py, yt, pw, pws, px, pxs, nb, out_dim, in_dim, _stream(stream)))
     return out
 
@@ -604,12 +597,28 @@ def gemm_fp8_gate_up_silu(w, w_scale, x, x_scale, q: torch.Tensor | None = None,
     inter gate rows, then the up rows; inter is a multiple of 128."""
     nb, in_dim = _dims(x, "x")
     inter = _dims(w, "w")[0] // 2
-    q, scale, qs = _fp8_rows(stream, q, scale, nb, inter, x)
-    _, _, xs = _fp8_rows(stream, x, x_scale, nb, in_dim, x, "x", "x_scale")
-    pq, ps, pw, pws, px, pxs = _ptrs(*qs, *_fp8_mat(w, w_scale, 2 * inter, in_dim), *xs)
+    q, qs = _out(q, "q", _F8, (nb, inter), _E4M3, x, stream)
+    scale, ss = _out(scale, "scale", _F32, (nb, (inter + 127) // 128), torch.float32, x, stream)
+    blocks = (in_dim + 127) // 128
+    pq, ps, pw, pws, px, pxs = _ptrs(qs, ss, (w, "w", _F8, (2 * inter, in_dim)),
+                                     (w_scale, "w_scale", _F32, ((2 * inter + 127) // 128, blocks)),
+                                     (x, "x", _F8, None), (x_scale, "x_scale", _F32, (nb, blocks)))
     _check("q4a_gemm_fp8_gate_up_silu", _lib.q4a_gemm_fp8_gate_up_silu(pq, ps, pw, pws, px, pxs, nb, inter, in_dim,
                                                                        _stream(stream)))
     return q, scale
+
+
+def _residual(residual, x_new, want_x_new: bool, nb: int, dim: int, x, stream):
+    """(q4a_type, spec, x_new, spec of x_new) of an optional residual."""
+    if residual is None:
+        if x_new is not None:
+            raise ValueError("x_new needs a residual")
+        return 0, None, None, None
+    rt = _type(residual, "residual")
+    ns = None
+    if x_new is not None or want_x_new:
+        x_new, ns = _out(x_new, "x_new", (residual.dtype,), (nb, dim), residual.dtype, x, stream)
+    return rt, (residual, "residual", None, (nb, dim)), x_new, ns
 
 
 def mlp_fp8(x, norm_w, w_gu, ws_gu, w_dn, ws_dn, residual: torch.Tensor | None = None, eps: float = 1e-6,
@@ -622,20 +631,16 @@ def mlp_fp8(x, norm_w, w_gu, ws_gu, w_dn, ws_dn, residual: torch.Tensor | None =
     inter = _dims(w_gu, "w_gu")[0] // 2
     xt = _type(x, "x")
     yt = _type(out_dtype if out is None else out, "y")
-    out = _empty_on(stream, (nb, hidden), out_dtype, x) if out is None else out
-    _, _, ns = _fp8_rows(stream, *(n or (None, None)), nb, hidden, x, "n", "n_scale")
-    _, _, hs = _fp8_rows(stream, *(h or (None, None)), nb, inter, x, "h", "h_scale")
-    rt = 0
-    if residual is not None:
-        rt = _type(residual, "residual")
-        if x_new is None and want_x_new:
-            x_new = _empty_on(stream, (nb, hidden), residual.dtype, x)
-    elif x_new is not None:
-        raise ValueError("x_new needs a residual")
+    out, ys = _out(out, "y", None, (nb, hidden), out_dtype, x, stream)
+    rt, rs, x_new, xs = _residual(residual, x_new, want_x_new, nb, hidden, x, stream)
+    nq, nsc = n or (None, None)
+    hq, hsc = h or (None, None)
+    nq, nqs = _out(nq, "n", _F8, (nb, hidden), _E4M3, x, stream)
+    nsc, nss = _out(nsc, "n_scale", _F32, (nb, (hidden + 127) // 128), torch.float32, x, stream)
+    hq, hqs = _out(hq, "h", _F8, (nb, inter), _E4M3, x, stream)
+    hsc, hss = _out(hsc, "h_scale", _F32, (nb, (inter + 127) // 128), torch.float32, x, stream)
     py, pxn, pn, pns, ph, phs, px, pr, pw, pgu, psg, pdn, psd = _ptrs(
-        (out, "y", None, (nb, hidden)), None if x_new is None else (x_new, "x_new", (residual.dtype,), (nb, hidden)),
-        *ns, *hs, (x, "x", None, None), None if residual is None else (residual, "residual", None, (nb, hidden)),
-        (norm_w, "norm_w", _BF16, (hidden,)), *_fp8_mat(w_gu, ws_gu, 2 * inter, hidden, "w_gu", "ws_gu"),
+        ys, xs, nqs, nss, hqs, hss, (x, "x", None, None), rs, (norm_w, "norm_w", _BF16, (hidden,)), *_fp8_mat(w_gu, ws_gu, 2 * inter, hidden, "w_gu", "ws_gu"),
         *_fp8_mat(w_dn, ws_dn, hidden, inter, "w_dn", "ws_dn"))
     _check("q4a_mlp_fp8", _lib.q4a_mlp_fp8(py, yt, pxn, pn, pns, ph, phs, px, xt, pr, rt, pw, float(eps), float(shift),
                                            pgu, psg, pdn, psd, nb, hidden, inter, _stream(stream)))

@@ -303,7 +303,7 @@ q4a_status launch_rows_x(const Fp8Norm& n, cudaStream_t stream) {
 // the rounded multiply-add): a group's largest magnitude is at its smallest or largest code, found on
 // pairs of codes where they lie in the packed word. And a group has 16 possible results: the lane
 // rounds those to e4m3, and a code becomes its byte by permutes over that table. 151936 x 4096 takes
-// 172 us (5.7 TB/s); with both passes on single weights it took 322 us.
+// 167 us (5.8 TB/s); with both passes on single weights it took 322 us.
 constexpr int kDqCols = 256;
 
 // Smallest and largest code of eight packed words. Field f of a word's halves is compared in place:
@@ -392,8 +392,7 @@ __global__ void __launch_bounds__(256)
             t[k] = e4m3x4(v[0], v[1], v[2], v[3]);
         }
         const int64_t row = row0 + 8 * i;
-        const bool on = col_on && row < rows;
-        uint4* dst = reinterpret_cast<uint4*>(w8 + row * in_dim + col);
+        uint4 res[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             uint32_t out[4];
@@ -403,8 +402,27 @@ __global__ void __launch_bounds__(256)
                 out[2 * h] = table_bytes(low3, bit3, t[0], t[1], t[2], t[3]);
                 out[2 * h + 1] = table_bytes(low3 >> 16, bit3 >> 16, t[0], t[1], t[2], t[3]);
             }
-            if (on) dst[k] = make_uint4(out[0], out[1], out[2], out[3]);
+            res[k] = make_uint4(out[0], out[1], out[2], out[3]);
         }
+        // a 4 x 4 transpose over the row's lanes, so that they store 64 neighbouring bytes at a time
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            const bool up = part & o;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k & o) continue;
+                uint4 v = up ? res[k] : res[k | o];
+                v.x = __shfl_xor_sync(0xffffffffu, v.x, o);
+                v.y = __shfl_xor_sync(0xffffffffu, v.y, o);
+                v.z = __shfl_xor_sync(0xffffffffu, v.z, o);
+                v.w = __shfl_xor_sync(0xffffffffu, v.w, o);
+                (up ? res[k] : res[k | o]) = v;
+            }
+        }
+        uint4* dst = reinterpret_cast<uint4*>(w8 + row * in_dim + ct * kDqCols) + part;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (row < rows && ct * kDqCols + k * kGroup < in_dim) dst[4 * k] = res[k];
     }
 }
 
