@@ -638,6 +638,17 @@ q4a_status check_gate_up_fp8(const Fp8Gemm& g) {
     return aligned(g.q, 16) && aligned(g.scale, 4) ? Q4A_OK : Q4A_ERR_ALIGN;
 }
 
+// A launcher behind the C boundary: host memory that runs out (the launchers keep per-device caches)
+// becomes a status, not an exception in the caller's frames.
+template <typename F>
+q4a_status launched(F f) {
+    try {
+        return f();
+    } catch (...) {
+        return cuda_fail(cudaErrorMemoryAllocation);
+    }
+}
+
 }  // namespace
 }  // namespace q4a
 
@@ -657,7 +668,7 @@ q4a_status q4a_quantize_fp8(uint8_t* q, float* scale, const void* x, q4a_type x_
     n.x_type = x_type;
     n.nb = nb;
     n.dim = dim;
-    return launch_fp8_rows(n, (cudaStream_t)stream);
+    return launched([&] { return launch_fp8_rows(n, (cudaStream_t)stream); });
 }
 
 q4a_status q4a_add_rmsnorm_fp8(uint8_t* q, float* scale, void* x_new, const void* x, q4a_type x_type,
@@ -665,7 +676,7 @@ q4a_status q4a_add_rmsnorm_fp8(uint8_t* q, float* scale, void* x_new, const void
                                float shift, int64_t nb, int64_t dim, q4a_stream_t stream) {
     const Fp8Norm n = {q, scale, x_new, x, x_type, residual, res_type, norm_w, eps, shift, nb, dim};
     const q4a_status st = check_add_rmsnorm(n);
-    return st != Q4A_OK ? st : launch_fp8_rows(n, (cudaStream_t)stream);
+    return st != Q4A_OK ? st : launched([&] { return launch_fp8_rows(n, (cudaStream_t)stream); });
 }
 
 q4a_status q4a_dequant_fp8(uint8_t* w8, float* w_scale, const uint8_t* w, const uint16_t* s, const uint16_t* b,
@@ -675,14 +686,14 @@ q4a_status q4a_dequant_fp8(uint8_t* w8, float* w_scale, const uint8_t* w, const 
     if (st != Q4A_OK) return st;
     if (!aligned(w8, 16) || !aligned(w_scale, 4) || !aligned(w, 16) || !aligned(s, 2) || !aligned(b, 2))
         return Q4A_ERR_ALIGN;
-    return launch_dequant_fp8(w8, w_scale, w, s, b, rows, in_dim, (cudaStream_t)stream);
+    return launched([&] { return launch_dequant_fp8(w8, w_scale, w, s, b, rows, in_dim, (cudaStream_t)stream); });
 }
 
 q4a_status q4a_gemm_fp8(void* y, q4a_type y_type, const uint8_t* w, const float* w_scale, const uint8_t* x,
                         const float* x_scale, int64_t nb, int64_t out_dim, int64_t in_dim, q4a_stream_t stream) {
     const Fp8Gemm g = {y, y_type, nullptr, nullptr, w, w_scale, x, x_scale, nb, out_dim, in_dim};
     const q4a_status st = check_gemm_fp8(g);
-    return st != Q4A_OK ? st : launch_gemm_fp8(g, (cudaStream_t)stream);
+    return st != Q4A_OK ? st : launched([&] { return launch_gemm_fp8(g, (cudaStream_t)stream); });
 }
 
 q4a_status q4a_gemm_fp8_gate_up_silu(uint8_t* q, float* scale, const uint8_t* w, const float* w_scale,
@@ -690,7 +701,7 @@ q4a_status q4a_gemm_fp8_gate_up_silu(uint8_t* q, float* scale, const uint8_t* w,
                                      int64_t in_dim, q4a_stream_t stream) {
     const Fp8Gemm g = {nullptr, Q4A_F32, q, scale, w, w_scale, x, x_scale, nb, inter, in_dim};
     const q4a_status st = check_gate_up_fp8(g);
-    return st != Q4A_OK ? st : launch_gemm_fp8(g, (cudaStream_t)stream);
+    return st != Q4A_OK ? st : launched([&] { return launch_gemm_fp8(g, (cudaStream_t)stream); });
 }
 
 q4a_status q4a_mlp_fp8(void* y, q4a_type y_type, void* x_new, uint8_t* n, float* n_scale, uint8_t* h,
@@ -704,10 +715,12 @@ q4a_status q4a_mlp_fp8(void* y, q4a_type y_type, void* x_new, uint8_t* n, float*
     q4a_status st = check_add_rmsnorm(norm);
     if (st == Q4A_OK) st = check_gate_up_fp8(gu);
     if (st == Q4A_OK) st = check_gemm_fp8(dn);
-    if (st == Q4A_OK) st = launch_fp8_rows(norm, (cudaStream_t)stream);
-    if (st == Q4A_OK) st = launch_gemm_fp8(gu, (cudaStream_t)stream);
-    if (st == Q4A_OK) st = launch_gemm_fp8(dn, (cudaStream_t)stream);
-    return st;
+    if (st != Q4A_OK) return st;
+    return launched([&] {
+        q4a_status s = launch_fp8_rows(norm, (cudaStream_t)stream);
+        if (s == Q4A_OK) s = launch_gemm_fp8(gu, (cudaStream_t)stream);
+        return s == Q4A_OK ? launch_gemm_fp8(dn, (cudaStream_t)stream) : s;
+    });
 }
 
 q4a_status q4a_check_device_error(q4a_stream_t stream) {

@@ -372,7 +372,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     const int64_t col = col0 + 16 * c;
-                    if (lane == 0 && row0 < p.g.nb && col < p.g.out_dim) tma_store_2d(&p.tmap_y, half, (int)col, (int)row0);
+                    if (lane == 0) {
+                        if (row0 < p.g.nb && col < p.g.out_dim) tma_store_2d(&p.tmap_y, half, (int)col, (int)row0);
+                        else asm volatile("cp.async.bulk.commit_group;" ::: "memory");   // keeps the count of boxes
+                    }
                 }
             } else {
                 // rows that no tensor store can reach: 16 columns at a time through the box, so that

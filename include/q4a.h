@@ -416,7 +416,8 @@ Q4A_API q4a_status q4a_moe_combine(float* out, const float* y, const int32_t* sl
  *   NaN code and leaves its block's scale to the other values; an infinity makes its block's
  *   scale infinite: either comes out of a product as NaN.
  *   Rows are multiples of 16 bytes: dim, in_dim and inter are multiples of 16 (the products fetch
- *   them with tensor copies).
+ *   them with tensor copies). An output overlaps neither an input nor another output, but for x_new
+ *   where it says so.
  *
  * q4a_quantize_fp8 -- activations in 8 bits.
  *   q      out  e4m3 [nb][dim]

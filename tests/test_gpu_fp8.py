@@ -11,8 +11,9 @@ Bars, from the arithmetic:
   magnitudes each), then a rounded scale product and one fused multiply-add per block:
   (128 * 2^-23 + (blocks + 2) * 2^-24) * sum |x w|, and the output's rounding;
 * the gated product: with those bounds eg, eu on g and u,
-  |dh| <= 1.1 (|u| + eu) eg + (|silu(g)| + 1.1 eg) eu + 2^-20 |h|  (silu' <= 1.1; expf, the
-  quotient and the product are a few roundings).
+  |dh| <= 1.1 (|u| + eu) eg + (|silu(g)| + 1.1 eg) eu + 2^-21 (1 + |g|) |h|  (silu' <= 1.1; the
+  fast exponential is off by 2 + 1.2 |g| units in the last place, 2^-23 each, the quotient by 2 and
+  the product by half of one).
 """
 
 import numpy as np
@@ -34,6 +35,7 @@ TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
 HALF_STEP = {"f32": 2.0 ** -24, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}
 TINY = {"f32": 1e-45, "f16": 2.0 ** -25, "bf16": 1e-40}
 NORM_TOL = 60 * U
+GATE_TOL = 2.0 ** -21
 
 
 def values(rng, shape, std=1.0):
@@ -137,6 +139,10 @@ def test_add_rmsnorm(nb, dim, t, rt):
         r2 = r.clone()
         q2, s2, same = q4a.add_rmsnorm_fp8(x, wd, residual=r2, eps=1e-5, shift=0.5, x_new=r2)
         assert same is r2 and np.array_equal(host64(r2), stored)
+        if rt == t:                                     # and on x, of the same type
+            x2 = x.clone()
+            q4, s4, same = q4a.add_rmsnorm_fp8(x2, wd, residual=r, eps=1e-5, shift=0.5, x_new=x2)
+            assert same is x2 and np.array_equal(host64(x2), stored) and torch.equal(bits(q4), bits(q))
         q3, s3, none = q4a.add_rmsnorm_fp8(x, wd, residual=r, eps=1e-5, shift=0.5, want_x_new=False)
         assert none is None
         for a, b in ((q, q2), (s, s2), (q, q3), (s, s3)):
@@ -311,13 +317,110 @@ def test_gemm_short_views():
         assert (np.abs(host64(y) - ref) <= err + HALF_STEP[t] * (np.abs(ref) + err)).all(), (nb, t)
 
 
+def device_reference(ops):
+    """product_reference for larger shapes: the operands' values (exact in 64 bits) multiplied in 64
+    bits on the device."""
+    w, ws, x, xs = (a.to(DEV) for a in ops)
+    wv = w.double() * ws.double().repeat_interleave(128, 0)[: w.shape[0]].repeat_interleave(128, 1)[:, : w.shape[1]]
+    xv = x.double() * xs.double().repeat_interleave(128, 1)[:, : x.shape[1]]
+    y, mag = xv @ wv.t(), xv.abs() @ wv.abs().t()
+    return y, (128 * 2.0 ** -23 + (xs.shape[1] + 2) * U) * mag
+
+
+def device_operands(gen, nb, out_dim, in_dim):
+    """Codes of every size and scales of both signs, made on the device."""
+    ops = []
+    for rows, blocks in ((out_dim, -(-out_dim // 128)), (nb, nb)):
+        codes = (torch.randn(rows, in_dim, device=DEV, generator=gen) * 100).clamp(-448, 448).to(F8)
+        ops += [codes, torch.randn(blocks, -(-in_dim // 128), device=DEV, generator=gen)]
+    return ops
+
+
+# Shapes that fill the GPU with 256 x 256 tiles: one block and less of one, block counts that are
+# and are not multiples of four, ragged rows and columns, and a y that no tensor store can reach.
+WIDE = [(8191, 8200, 128), (8192, 8192, 16), (5000, 8192, 272), (1024, 12288, 512), (2047, 12304, 640),
+        (3000, 4096, 1296), (700, 12296, 2048), (4095, 4098, 8192)]
+
+
+@pytest.mark.parametrize("t", sorted(TYPES))
+@pytest.mark.parametrize("nb,out_dim,in_dim", WIDE)
+def test_gemm_many_rows(nb, out_dim, in_dim, t):
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(nb + out_dim + in_dim)
+    ops = device_operands(gen, nb, out_dim, in_dim)
+    big, y = guarded((nb, out_dim), TYPES[t], float("nan"))
+    q4a.gemm_fp8(*ops, out=y)
+    torch.cuda.synchronize()
+    q4a.check_device_error()
+    ref, err = device_reference(ops)
+    scale = 65504.0 / 4 / float(ref.abs().max()) if t == "f16" and ref.abs().max() > 65504 else 1.0
+    if scale < 1.0:                                    # within binary16: the same case with smaller scales
+        ops[3] = ops[3] * 2.0 ** np.floor(np.log2(scale))
+        q4a.gemm_fp8(*ops, out=y)
+        ref, err = device_reference(ops)
+    bound = err + HALF_STEP[t] * (ref.abs() + err) + TINY[t]
+    assert torch.isfinite(y).all(), "non-finite or unwritten"
+    worst = float(((y.double() - ref).abs() / bound).max())
+    assert worst <= 1.0, f"gemm {nb} x {in_dim} -> {out_dim} {t}: off by {worst:.3g} of the bound"
+    check_guard(big, nb, "rows behind the last")
+
+
+@pytest.mark.parametrize("nb,inter,in_dim", [(3000, 6144, 272), (8191, 4096, 128), (1111, 6144, 1040), (4096, 2048, 16)])
+def test_gate_up_many_rows(nb, inter, in_dim):
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(nb + inter + in_dim)
+    ops = device_operands(gen, nb, 2 * inter, in_dim)
+    ops[1] *= 2.0 ** -14                               # gates of a few units
+    bq, q = guarded((nb, inter), F8, 2.0)
+    bs, s = guarded((nb, inter // 128), torch.float32, 3.0)
+    q4a.gemm_fp8_gate_up_silu(*ops, q=q, scale=s)
+    torch.cuda.synchronize()
+    q4a.check_device_error()
+    y, err = device_reference(ops)
+    g, u, eg, eu = y[:, :inter], y[:, inter:], err[:, :inter], err[:, inter:]
+    sg = g * torch.sigmoid(g)
+    h = sg * u
+    e = 1.1 * (u.abs() + eu) * eg + (sg.abs() + 1.1 * eg) * eu + GATE_TOL * (1 + g.abs()) * h.abs()
+    some = torch.cat((torch.arange(0, nb, 7), torch.arange(nb - 5, nb))).unique().to(DEV)   # every 7th row and the last
+    check_codes(q[some], s[some], host64(h[some]), f"gate_up {nb} x {in_dim} -> {inter}", err=host64(e[some]))
+    check_guard(bq, nb, "codes behind the last row")
+    check_guard(bs, nb, "scales behind the last row")
+
+
+def test_many_rows_nan_stays_in_its_rows():
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(77)
+    ops = device_operands(gen, 2000, 8192, 400)
+    clean = q4a.gemm_fp8(*ops)
+    ops[2].view(torch.uint8)[1333, 7] = 0x7F
+    ops[0].view(torch.uint8)[4100, 390] = 0xFF
+    y = q4a.gemm_fp8(*ops)
+    assert torch.isnan(y[1333]).all() and torch.isnan(y[:, 4100]).all()
+    keep = torch.ones_like(y, dtype=torch.bool)
+    keep[1333], keep[:, 4100] = False, False
+    assert torch.equal(y[keep], clean[keep])
+
+
+@pytest.mark.parametrize("nb", [2000, 4096])
+def test_many_rows_repeatable(nb):
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(nb)
+    ops = device_operands(gen, nb, 8192, 1024)
+    ops[1] *= 2.0 ** -14
+    first, (q, s) = q4a.gemm_fp8(*ops), q4a.gemm_fp8_gate_up_silu(*ops)
+    for _ in range(5):
+        assert torch.equal(q4a.gemm_fp8(*ops), first)
+        q2, s2 = q4a.gemm_fp8_gate_up_silu(*ops)
+        assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s, s2)
+
+
 def gated_reference(ops):
     y, err = product_reference(ops)
     half = y.shape[1] // 2
     g, u, eg, eu = y[:, :half], y[:, half:], err[:, :half], err[:, half:]
     sg = g / (1 + np.exp(-g))
     h = sg * u
-    return h, 1.1 * (np.abs(u) + eu) * eg + (np.abs(sg) + 1.1 * eg) * eu + 2.0 ** -20 * np.abs(h)
+    return h, 1.1 * (np.abs(u) + eu) * eg + (np.abs(sg) + 1.1 * eg) * eu + GATE_TOL * (1 + np.abs(g)) * np.abs(h)
 
 
 @pytest.mark.parametrize("nb,inter,in_dim", [(1, 128, 64), (2, 128, 16), (3, 256, 528), (9, 640, 2048), (16, 384, 272),
