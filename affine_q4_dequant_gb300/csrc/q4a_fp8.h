@@ -52,8 +52,9 @@ struct Fp8Gemm {
 q4a_status launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t stream);
 q4a_status read_and_clear_gemm_fp8_error(uint32_t* word);   // after a stream synchronisation
 
-// The form for many activation rows (q4a_fp8_wide.cu).
-q4a_status launch_gemm_fp8_wide(const Fp8Gemm& g, cudaStream_t stream);
+// The form for many activation rows (q4a_fp8_wide.cu); split: two pairs of SMs a tile (at least 8 column
+// blocks).
+q4a_status launch_gemm_fp8_wide(const Fp8Gemm& g, bool split, cudaStream_t stream);
 bool fp8_wide_tma_y(const Fp8Gemm& g);   // whether its y can leave through tensor stores
 q4a_status read_and_clear_fp8_wide_error(uint32_t* word);
 

@@ -51,8 +51,12 @@ constexpr int kNwMaxCluster = 8;
 //   gated 4096 -> 6144      8 rows, N 16, C 3 / 5 / 6: 12.9 / 12.8 / 17.8;
 //                           64 rows, N 64, C 1 / 2: 19.2 / 14.3; N 32, C 3: 15.6; wide: 17.7
 //   4096 -> 12288           wide, 256 / 512 / 1024 rows: 18.1 / 31.2 / 45.0; N 128: 28 and more
-constexpr float kNwBytesPerUs = 9.0e6f, kNwFixedUs = 3.2f, kNwRowUs = 0.006f, kNwSplitUs = 1.0f;
-constexpr float kWdFixedUs = 2.8f, kWdTileUs = 1.2f, kWdScalarUs = 8.f, kWdBlockUs = 0.40f;
+//   12288 -> 4096, 512 rows wide: 39.5, split: 28.2; N 128: 37.2
+//   gated 6208 -> 2176, 300 rows  wide: 25.3, split: 20.4; N 128, C 2: 24.1
+constexpr float kNwBytesPerUs = 9.0e6f, kNwFixedUs = 3.2f, kNwRowUs = 0.006f, kNwSplitUs = 1.0f,
+                kNwWaveUs = 1.0f, kNwWaveRowUs = 0.02f;
+constexpr float kWdFixedUs = 2.8f, kWdTileUs = 1.2f, kWdScalarUs = 3.f, kWdBlockUs = 0.40f,
+                kWdSplitUs = 6.f;
 
 constexpr int pow2_at_least(int v) {
     int p = 32;
@@ -158,6 +162,10 @@ __device__ __forceinline__ void add_block(float2 (&acc)[CPT / 2], uint32_t taddr
             if (c + 1 < CPT / 16) tc_ld16_wait(d[(c + 1) & 1]);
         }
     }
+}
+
+__device__ __forceinline__ uint32_t half_bits(float f, int type) {
+    return type == Q4A_F16 ? __half_as_ushort(__float2half_rn(f)) : __bfloat16_as_ushort(__float2bfloat16_rn(f));
 }
 
 template <int N, int T>
@@ -355,25 +363,30 @@ __global__ void __launch_bounds__(kNwThreads, Narrow<N, T>::R) narrow_kernel(con
                     e4m3x4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
                 if (lane == 0) p.g.scale[row * (p.g.out_dim / kFp8Block) + o0 / kFp8Block] = scale;
             } else {
-                const int64_t at = row * p.g.out_dim + o;
-                const float f[4] = {a.x, a.y, a.z, a.w};
-                if (p.g.y_type == Q4A_F32) {
-                    float* y = static_cast<float*>(p.g.y) + at;
-                    if (p.y_vec && o < p.g.out_dim) *reinterpret_cast<float4*>(y) = a;
+                const int64_t at = row * p.g.out_dim + o0;
+                if (p.y_vec) {
+                    if (o >= p.g.out_dim) continue;
+                    if (p.g.y_type == Q4A_F32) *reinterpret_cast<float4*>(static_cast<float*>(p.g.y) + at + 4 * lane) = a;
                     else
-                        for (int j = 0; j < 4; ++j)
-                            if (o + j < p.g.out_dim) y[j] = f[j];
+                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.g.y) + at + 4 * lane) =
+                            make_uint2(half_bits(a.x, p.g.y_type) | half_bits(a.y, p.g.y_type) << 16,
+                                       half_bits(a.z, p.g.y_type) | half_bits(a.w, p.g.y_type) << 16);
                 } else {
-                    uint16_t* y = static_cast<uint16_t*>(p.g.y) + at;
-                    uint16_t h[4];
-                    for (int j = 0; j < 4; ++j)
-                        h[j] = p.g.y_type == Q4A_F16 ? __half_as_ushort(__float2half_rn(f[j]))
-                                                     : __bfloat16_as_ushort(__float2bfloat16_rn(f[j]));
-                    if (p.y_vec && o < p.g.out_dim)
-                        *reinterpret_cast<uint2*>(y) = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
-                    else
-                        for (int j = 0; j < 4; ++j)
-                            if (o + j < p.g.out_dim) y[j] = h[j];
+                    // rows of any pitch: through this warp's own row of the ring, so that neighbouring
+                    // lanes write neighbouring elements
+                    const uint32_t mine = ring + (uint32_t)n * 512u;
+                    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(mine), "f"(a.x), "f"(a.y), "f"(a.z), "f"(a.w)
+                                 : "memory");
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float f;
+                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(mine - (uint32_t)lane * 12u + 128u * j));
+                        const int64_t c = 32 * j + lane;
+                        if (o0 + c >= p.g.out_dim) continue;
+                        if (p.g.y_type == Q4A_F32) static_cast<float*>(p.g.y)[at + c] = f;
+                        else static_cast<uint16_t*>(p.g.y)[at + c] = (uint16_t)half_bits(f, p.g.y_type);
+                    }
                 }
             }
         }
@@ -443,7 +456,8 @@ q4a_status plan_narrow(const Fp8Gemm& g, int dev, float lat, Fp8Plan* best) {
         const float running = (float)((tiles < slots[c] ? tiles : slots[c]) * c);
         const float feed = running * (float)Narrow<N, T>::stage / kNwBytesPerUs;
         const float us = kNwFixedUs + kNwRowUs * (float)(T * N) + (c > 1 ? kNwSplitUs : 0.f) +
-                         (float)waves * ((float)((nk + c - 1) / c) * (lat > feed ? lat : feed)) + (float)(waves - 1);
+                         (float)waves * ((float)((nk + c - 1) / c) * (lat > feed ? lat : feed)) +
+                         (float)(waves - 1) * (kNwWaveUs + kNwWaveRowUs * (float)(T * N));
         if (best->us == 0.f || us < best->us) *best = {N, c, us};
     }
     return Q4A_OK;
@@ -522,15 +536,23 @@ q4a_status launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t stream) {
     auto consider = [&](int n) { return st == Q4A_OK && (n == 16 || g.nb > n / 2) && (n == 128 || g.nb <= 8 * n); };
     if (consider(16)) st = gated_form ? plan_narrow<16, 2>(g, dev, 0.45f, &plan) : plan_narrow<16, 1>(g, dev, 0.29f, &plan);
     if (consider(32)) st = gated_form ? plan_narrow<32, 2>(g, dev, 0.6f, &plan) : plan_narrow<32, 1>(g, dev, 0.30f, &plan);
-    if (consider(64)) st = gated_form ? plan_narrow<64, 2>(g, dev, 0.45f, &plan) : plan_narrow<64, 1>(g, dev, 0.43f, &plan);
+    if (consider(64)) st = gated_form ? plan_narrow<64, 2>(g, dev, 0.50f, &plan) : plan_narrow<64, 1>(g, dev, 0.43f, &plan);
     if (consider(128)) st = gated_form ? plan_narrow<128, 2>(g, dev, 0.8f, &plan) : plan_narrow<128, 1>(g, dev, 0.4f, &plan);
     if (st != Q4A_OK) return st;
     {
+        const int* slots = nullptr;   // one CTA an SM, as the wide kernel
+        st = narrow_slots<128, 1>(dev, &slots);
+        if (st != Q4A_OK) return st;
         const int64_t nk = (g.in_dim + kFp8Block - 1) / kFp8Block;
         const int64_t tiles = (g.nb + 255) / 256 * (gated_form ? g.out_dim / 128 : (g.out_dim + 255) / 256);
-        const float waves = (float)((tiles + sms / 2 - 1) / (sms / 2));
-        const float tile = kWdTileUs + (gated_form || fp8_wide_tma_y(g) ? 0.f : kWdScalarUs) + kWdBlockUs * (float)nk;
-        if (kWdFixedUs + waves * tile < plan.us) return launch_gemm_fp8_wide(g, stream);
+        const float out = kWdTileUs + (gated_form || fp8_wide_tma_y(g) ? 0.f : kWdScalarUs);
+        const float whole = kWdFixedUs + (float)((tiles + sms / 2 - 1) / (sms / 2)) * (out + kWdBlockUs * (float)nk);
+        float split = whole;
+        if (nk >= 8 && slots[4] > 0)
+            split = kWdFixedUs + (float)((tiles + slots[4] - 1) / slots[4]) *
+                                     (out + kWdSplitUs + kWdBlockUs * (float)(nk - nk / 2 / 4 * 4));
+        if (split < whole && split < plan.us) return launch_gemm_fp8_wide(g, true, stream);
+        if (whole < plan.us) return launch_gemm_fp8_wide(g, false, stream);
     }
     if (gated_form) {
         if (plan.n == 16) return launch_narrow<16, 2>(g, plan.cluster, stream);

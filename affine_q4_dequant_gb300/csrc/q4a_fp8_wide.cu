@@ -9,7 +9,8 @@
 // fp32): two accumulators fill the TMEM. cta_group::2 lets each SM hold half of the weights' tile:
 // a lone SM would read 48 KB of shared memory a block, 32 KB here.
 //
-// CTA (320 threads; two of them a cluster, one persistent cluster per SM pair):
+// CTA (320 threads; two of them a cluster, one persistent cluster per SM pair, or four, two pairs on one
+// tile):
 //   warp 0      TMA producer of this CTA's 128 activation rows and 128 weight rows of a block,
 //               signalled on the leader's barrier; the rows' and the tile's scales by cp.async
 //   warp 1      allocates TMEM; in the leader issues the MMAs of both CTAs
@@ -56,6 +57,7 @@ struct WideParams {
     Fp8Gemm g;
     int32_t nk;            // column blocks
     int32_t m_tiles, n_tiles;
+    int32_t k_split;       // first column block of the second pair (kernels with SPLIT; a multiple of 4)
     int32_t xs_vec;        // rows of x_scale allow 16-byte copies
 };
 
@@ -68,9 +70,9 @@ __device__ __forceinline__ void wd_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
 }
 // The address of the leader's copy of a shared variable.
-__device__ __forceinline__ uint32_t leader_addr(uint32_t addr) {
+__device__ __forceinline__ uint32_t leader_addr(uint32_t addr, uint32_t leader) {
     uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(leader));
     return r;
 }
 // Tells the leader that an accumulator has been read. The reads are complete (tcgen05.wait::ld) and
@@ -106,16 +108,13 @@ __device__ __forceinline__ void wd_mma(uint32_t d_tmem, uint64_t adesc, uint64_t
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// Arrives on the barrier of both CTAs once the MMAs issued before have completed.
-__device__ __forceinline__ void wd_commit(uint32_t bar) {
+// Arrives on the barrier of the pair's CTAs (a mask of cluster ranks) once the MMAs issued before have
+// completed.
+__device__ __forceinline__ void wd_commit(uint32_t bar, uint16_t pair_mask) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
+        "h"(pair_mask)
         : "memory");
-}
-
-__device__ __forceinline__ void sts_f32(uint32_t addr, float v) {
-    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 // Tile t: groups of 8 row tiles pass over all weight tiles, so the pairs at work share both.
@@ -126,9 +125,8 @@ __device__ __forceinline__ void tile_at(const WideParams& p, int t, int64_t& m0,
     nt = in / rows;
 }
 
-// How the tile leaves: the gated form's 8-bit rows; y through shared memory and tensor stores, by its
-// type; or y element by element.
-enum WideOut : int { kWdGated, kWdF32, kWdF16, kWdBf16, kWdScalar };
+// How the tile leaves: the gated form's 8-bit rows, or y by its type.
+enum WideOut : int { kWdGated, kWdF32, kWdF16, kWdBf16 };
 
 template <WideOut OUT>
 __device__ __forceinline__ uint32_t pack_y(float a, float b) {
@@ -140,8 +138,38 @@ __device__ __forceinline__ uint32_t pack_y(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// A box's 32 rows of 64 bytes to y, half a warp a row: rows that no tensor store can reach (their pitch
+// or base is no multiple of 16 bytes). 4 bytes a lane where the address allows, else by element (shifting
+// such a row's elements between lanes to 4-byte stores was slower: 43.7 against 36.2 us for 644 rows of
+// 9287 outputs).
 template <WideOut OUT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
+__device__ __forceinline__ void rows_out(const Fp8Gemm& g, uint32_t box, int64_t row0, int64_t col, int lane) {
+    constexpr int size = OUT == kWdF32 ? 4 : 2;
+    const int64_t c = col + (lane & 15) * (4 / size);          // first element of this lane
+    const int rows = (int)(g.nb - row0 < 32 ? g.nb - row0 : 32);
+    const int n = c >= g.out_dim ? 0 : (size == 2 && c + 1 < g.out_dim ? 2 : 1);   // elements of this lane
+    uint8_t* y = static_cast<uint8_t*>(g.y) + ((row0 + (lane >> 4)) * g.out_dim + c) * size;
+    const int64_t step = 2 * g.out_dim * size;
+    if (n == 0) return;
+#pragma unroll 4
+    for (int r = lane >> 4; r < rows; r += 2, y += step) {
+        uint32_t v;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v)
+                     : "r"(box + (uint32_t)r * 64u + ((((uint32_t)(lane & 15) >> 2) ^ (((uint32_t)r >> 1) & 3u)) << 4) +
+                           ((uint32_t)lane & 3u) * 4u));
+        if (size == 4 || (n == 2 && (reinterpret_cast<uintptr_t>(y) & 3) == 0)) {
+            *reinterpret_cast<uint32_t*>(y) = v;
+        } else {
+            reinterpret_cast<uint16_t*>(y)[0] = (uint16_t)v;
+            if (n == 2) reinterpret_cast<uint16_t*>(y)[1] = (uint16_t)(v >> 16);
+        }
+    }
+}
+
+// TMA_Y: y leaves by tensor stores (16-byte rows); else its rows are written from the boxes.
+// SPLIT: two pairs of SMs share a tile, each with half of its column blocks (few tiles, long rows).
+template <WideOut OUT, bool TMA_Y, bool SPLIT>
+__global__ void __launch_bounds__(kWdThreads, 1)
     wide_kernel(const __grid_constant__ WideParams p) {
     constexpr bool GATED = OUT == kWdGated;
     extern __shared__ uint8_t smem_raw[];
@@ -154,8 +182,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + kWdAbort);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)wd_rank();
-    const int pairs = (int)(gridDim.x >> 1), pair = (int)(blockIdx.x >> 1);
+    const int pairs = (int)(gridDim.x >> (SPLIT ? 2 : 1)), pair = (int)(blockIdx.x >> (SPLIT ? 2 : 1));
     const int tiles = p.m_tiles * p.n_tiles, nk = p.nk;
+    // this pair's column blocks (whole groups of four scales) and the rank of its leader
+    const int kb0 = SPLIT && rank >= 2 ? p.k_split : 0, kb1 = SPLIT && rank < 2 ? p.k_split : nk;
+    const uint32_t leader = SPLIT ? (uint32_t)rank & 2u : 0u;
+    const int side = SPLIT ? rank & 1 : rank;   // which CTA of the pair
+    const bool leads = side == 0;
 
     grid_dep_launch();
     if (threadIdx.x == 0) {
@@ -192,17 +225,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
             int64_t m0;
             int nt;
             tile_at(p, t, m0, nt);
-            m0 += rank * 128;
-            const int64_t wrow = GATED ? rank * p.g.out_dim + (int64_t)nt * 128 : (int64_t)nt * 256 + rank * 128;
+            m0 += side * 128;
+            const int64_t wrow = GATED ? side * p.g.out_dim + (int64_t)nt * 128 : (int64_t)nt * 256 + side * 128;
             // the weight blocks of the tile's two column halves (a half beyond out_dim: any factor)
             const int64_t wb0 = GATED ? (int64_t)nt : (int64_t)nt * 2;
             const int64_t wb1 = GATED ? p.g.out_dim / kFp8Block + nt
                                       : (wb0 + 1 < (p.g.out_dim + 127) / 128 ? wb0 + 1 : wb0);
-            for (int kb = 0; kb < nk; ++kb) {
+            for (int kb = kb0; kb < kb1; ++kb) {
                 mbar_wait(empty + 8 * s, s_phase, abort_flag);
                 if (lane == 0) {
-                    if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * kWdStage);
-                    const uint32_t lf = leader_addr(full + 8 * s), at = base + s * kWdStage;
+                    if (leads) mbar_arrive_expect_tx(full + 8 * s, 2 * kWdStage);
+                    const uint32_t lf = leader_addr(full + 8 * s, leader), at = base + s * kWdStage;
                     wd_tma_load(at, &p.tmap_x, kb * kFp8Block, (int)m0, lf);
                     wd_tma_load(at + kWdTile, &p.tmap_w, kb * kFp8Block, (int)wrow, lf);
                 }
@@ -230,13 +263,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
+        if (SPLIT) wd_cluster_sync();   // the second pair's sums (see the adding warps)
     } else if (warp == 1) {
-        if (rank == 0) {
+        if (leads) {
             constexpr uint32_t idesc = idesc_f8(256, 256);
+            const uint16_t pair_mask = (uint16_t)(3u << leader);
             int s = 0;
             uint32_t s_phase = 0, buf = 0, buf_phase = 1;   // the first use of an accumulator finds it free
             for (int t = pair; t < tiles; t += pairs) {
-                for (int kb = 0; kb < nk; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     mbar_wait(full + 8 * s, s_phase, abort_flag);
                     mbar_wait(acc_empty + 8 * buf, buf_phase, abort_flag);
                     __syncwarp();
@@ -246,8 +281,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             wd_mma(tmem + (uint32_t)(buf * 256), ad + 2u * k, bd + 2u * k, idesc, (uint32_t)k);
-                        wd_commit(acc_full + 8 * buf);
-                        wd_commit(empty + 8 * s);
+                        wd_commit(acc_full + 8 * buf, pair_mask);
+                        wd_commit(empty + 8 * s, pair_mask);
                     }
                     __syncwarp();
                     if (++s == kWdS) s = 0, s_phase ^= 1;
@@ -255,6 +290,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                 }
             }
         }
+        __syncwarp();
+        if (SPLIT) wd_cluster_sync();
     } else {
         const int wg = (warp - kWdAdd0) >> 2, quarter = warp & 3;
         const int rl = quarter * 32 + lane;                  // row of this CTA's 128
@@ -262,14 +299,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
         // this thread's columns: two spans of 64
         const int span0 = GATED ? wg * 64 : wg * 128, span1 = GATED ? 128 + wg * 64 : wg * 128 + 64;
         const uint32_t box = base + kWdY + (uint32_t)(warp - kWdAdd0) * kWdBox;
-        const uint32_t free0 = leader_addr(acc_empty);
+        const uint32_t free0 = leader_addr(acc_empty, leader);
         int i = 0, sl = kWdSL - 1;
         uint32_t sl_phase = 1;
         float2 acc[64];
         for (int t = pair; t < tiles; t += pairs) {
 #pragma unroll
             for (int c = 0; c < 64; ++c) acc[c] = make_float2(0.f, 0.f);
-            for (int kb = 0; kb < nk; ++kb, ++i) {
+            for (int kb = kb0; kb < kb1; ++kb, ++i) {
                 const int buf = i & 1;
                 if ((kb & 3) == 0) {
                     if (++sl == kWdSL) sl = 0, sl_phase ^= 1;
@@ -303,11 +340,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                     if (c < 7) tc_ld16_wait(d[(c + 1) & 1]);
                 }
             }
+            if constexpr (SPLIT) {
+                // One tile a cluster. The second pair's sums go to the first through its ring (all of
+                // its blocks have been multiplied), [64][256 threads] pairs of columns.
+                const uint32_t at = base + (threadIdx.x - kWdAdd0 * 32) * 8u;
+                if (rank >= 2) {
+#pragma unroll
+                    for (int c = 0; c < 64; ++c)
+                        asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(at + 2048u * c), "f"(acc[c].x), "f"(acc[c].y)
+                                     : "memory");
+                }
+                wd_cluster_sync();
+                if (rank >= 2) break;
+                const uint32_t other = leader_addr(at, (uint32_t)rank + 2u);
+#pragma unroll
+                for (int c = 0; c < 64; ++c) {
+                    float x, y;
+                    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(x), "=f"(y) : "r"(other + 2048u * c));
+                    acc[c].x += x;
+                    acc[c].y += y;
+                }
+            }
             int64_t m0;
             int nt;
             tile_at(p, t, m0, nt);
             if (GATED) {
-                const int64_t row = m0 + rank * 128 + rl;
+                const int64_t row = m0 + side * 128 + rl;
                 float amax = 0.f;
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
@@ -336,17 +394,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                     }
                     if (wg == 0) p.g.scale[row * (p.g.out_dim / kFp8Block) + nt] = scale;
                 }
-            } else if (OUT != kWdScalar) {
+            } else {
                 // 64 bytes of a row at a time through one of this warp's two boxes (16-byte unit u of row
-                // r at u ^ (r / 2 & 3)), rows and columns beyond y clipped by the tensor map
-                const int64_t col0 = (int64_t)nt * 256 + wg * 128, row0 = m0 + rank * 128 + quarter * 32;
+                // r at u ^ (r / 2 & 3)): a tensor store clips rows and columns beyond y
+                const int64_t col0 = (int64_t)nt * 256 + wg * 128, row0 = m0 + side * 128 + quarter * 32;
                 constexpr bool f32 = OUT == kWdF32;
                 const uint32_t line = (uint32_t)lane * 64u, sw = ((uint32_t)lane >> 1) & 3u;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {       // 16 columns of 4 bytes, or 32 of 2
                     if (!f32 && (c & 1)) continue;
                     const uint32_t half = box + (uint32_t)((f32 ? c : c / 2) & 1) * (kWdBox / 2);
-                    if (lane == 0) bulk_wait_read_1();
+                    if (TMA_Y && lane == 0) bulk_wait_read_1();
                     __syncwarp();
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
@@ -369,48 +427,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                                          : "memory");
                         }
                     }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
                     const int64_t col = col0 + 16 * c;
-                    if (lane == 0) {
-                        if (row0 < p.g.nb && col < p.g.out_dim) tma_store_2d(&p.tmap_y, half, (int)col, (int)row0);
-                        else asm volatile("cp.async.bulk.commit_group;" ::: "memory");   // keeps the count of boxes
-                    }
-                }
-            } else {
-                // rows that no tensor store can reach: 16 columns at a time through the box, so that
-                // half a warp writes neighbouring elements of a row
-                const int64_t col0 = (int64_t)nt * 256 + wg * 128 + (lane & 15), row0 = m0 + rank * 128 + quarter * 32;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    __syncwarp();
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        sts_f32(box + (uint32_t)(lane * 17 + 2 * k) * 4u, acc[8 * c + k].x);
-                        sts_f32(box + (uint32_t)(lane * 17 + 2 * k + 1) * 4u, acc[8 * c + k].y);
-                    }
-                    __syncwarp();
-#pragma unroll 4
-                    for (int r = lane >> 4; r < 32; r += 2) {
-                        float f;
-                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(box + (uint32_t)(r * 17 + (lane & 15)) * 4u));
-                        if (row0 + r < p.g.nb && col0 + 16 * c < p.g.out_dim) {
-                            const int64_t at = (row0 + r) * p.g.out_dim + col0 + 16 * c;
-                            if (p.g.y_type == Q4A_F32) static_cast<float*>(p.g.y)[at] = f;
-                            else if (p.g.y_type == Q4A_F16) static_cast<__half*>(p.g.y)[at] = __float2half_rn(f);
-                            else static_cast<__nv_bfloat16*>(p.g.y)[at] = __float2bfloat16_rn(f);
+                    if constexpr (TMA_Y) {
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (row0 < p.g.nb && col < p.g.out_dim) tma_store_2d(&p.tmap_y, half, (int)col, (int)row0);
+                            else asm volatile("cp.async.bulk.commit_group;" ::: "memory");   // keeps the count of boxes
                         }
+                    } else {
+                        __syncwarp();
+                        rows_out<OUT>(p.g, half, row0, col, lane);
                     }
                 }
             }
         }
-        if (lane == 0) bulk_wait_all();   // no CTA exits while its y stores read shared memory
+        if (TMA_Y && lane == 0) bulk_wait_all();   // no CTA exits while its y stores read shared memory
     }
 
     // after a give-up no one has waited for the last copies and MMAs: they may not outlive the CTA
-    if (*abort_flag && warp == 1 && rank == 0) {
+    if (*abort_flag && warp == 1 && leads) {
         int n = 0;
-        for (int t = pair; t < tiles; t += pairs) n += nk;
+        for (int t = pair; t < tiles; t += pairs) n += kb1 - kb0;
         for (int i = n < kWdS ? 0 : n - kWdS; i < n; ++i) mbar_drain(full + 8 * (i % kWdS), (uint32_t)(i / kWdS) & 1u);
         for (int i = n < 2 ? 0 : n - 2; i < n; ++i) mbar_drain(acc_full + 8 * (i & 1), (uint32_t)(i / 2) & 1u);
     }
@@ -429,7 +467,15 @@ bool fp8_wide_tma_y(const Fp8Gemm& g) {
     return row % 16 == 0 && reinterpret_cast<uintptr_t>(g.y) % 16 == 0 && g.nb >= 32 && row >= 64;
 }
 
-q4a_status launch_gemm_fp8_wide(const Fp8Gemm& g, cudaStream_t stream) {
+template <bool SPLIT>
+auto wide_out(const Fp8Gemm& g, bool tma_y) {
+    if (g.q) return wide_kernel<kWdGated, false, SPLIT>;
+    if (g.y_type == Q4A_F32) return tma_y ? wide_kernel<kWdF32, true, SPLIT> : wide_kernel<kWdF32, false, SPLIT>;
+    if (g.y_type == Q4A_F16) return tma_y ? wide_kernel<kWdF16, true, SPLIT> : wide_kernel<kWdF16, false, SPLIT>;
+    return tma_y ? wide_kernel<kWdBf16, true, SPLIT> : wide_kernel<kWdBf16, false, SPLIT>;
+}
+
+q4a_status launch_gemm_fp8_wide(const Fp8Gemm& g, bool split, cudaStream_t stream) {
     int dev = 0, sms = 0;
     q4a_status st = fp8_sm_count(&dev, &sms);
     if (st != Q4A_OK) return st;
@@ -464,23 +510,24 @@ q4a_status launch_gemm_fp8_wide(const Fp8Gemm& g, cudaStream_t stream) {
                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
         if (r != CUDA_SUCCESS) return cuda_fail_drv(r);
     }
-    auto kernel = gated_form ? wide_kernel<kWdGated>
-                  : !tma_y ? wide_kernel<kWdScalar>
-                  : g.y_type == Q4A_F32 ? wide_kernel<kWdF32>
-                  : g.y_type == Q4A_F16 ? wide_kernel<kWdF16> : wide_kernel<kWdBf16>;
+    p.k_split = (p.nk / 2 + 3) / 4 * 4;
+    auto kernel = split ? wide_out<true>(g, tma_y) : wide_out<false>(g, tma_y);
     st = fp8_allow_smem(kernel, dev, kWdSmem);
     if (st != Q4A_OK) return st;
-    const int64_t tiles = m_tiles * n_tiles, pairs = sms / 2;
+    const int64_t tiles = m_tiles * n_tiles, pairs = sms / 2, cluster = split ? 4 : 2;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)), 1, 1);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(cluster * (split || tiles < pairs ? tiles : pairs)), 1, 1);   // split: a cluster a tile
     cfg.blockDim = dim3(kWdThreads, 1, 1);
     cfg.dynamicSmemBytes = kWdSmem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
     return e == cudaSuccess ? Q4A_OK : cuda_fail(e);
 }
