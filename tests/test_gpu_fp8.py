@@ -339,7 +339,9 @@ def device_operands(gen, nb, out_dim, in_dim):
 # Shapes that fill the GPU with 256 x 256 tiles: one block and less of one, block counts that are
 # and are not multiples of four, ragged rows and columns, and a y that no tensor store can reach.
 WIDE = [(8191, 8200, 128), (8192, 8192, 16), (5000, 8192, 272), (1024, 12288, 512), (2047, 12304, 640),
-        (3000, 4096, 1296), (700, 12296, 2048), (4095, 4098, 8192)]
+        (3000, 4096, 1296), (700, 12296, 2048), (4095, 4098, 8192),
+        # few tiles of long rows: two pairs of SMs a tile, halves of equal and of unequal lengths
+        (300, 4096, 8192), (511, 2304, 16384), (300, 4001, 6288), (1000, 520, 7696)]
 
 
 @pytest.mark.parametrize("t", sorted(TYPES))
@@ -365,7 +367,8 @@ def test_gemm_many_rows(nb, out_dim, in_dim, t):
     check_guard(big, nb, "rows behind the last")
 
 
-@pytest.mark.parametrize("nb,inter,in_dim", [(3000, 6144, 272), (8191, 4096, 128), (1111, 6144, 1040), (4096, 2048, 16)])
+@pytest.mark.parametrize("nb,inter,in_dim", [(3000, 6144, 272), (8191, 4096, 128), (1111, 6144, 1040), (4096, 2048, 16),
+                                             (300, 2176, 6208), (1006, 768, 8336)])
 def test_gate_up_many_rows(nb, inter, in_dim):
     gen = torch.Generator(device=DEV)
     gen.manual_seed(nb + inter + in_dim)
@@ -552,6 +555,30 @@ def test_two_streams_at_once():
         for (y, xn), (y0, x0) in zip(pair, alone):
             assert torch.equal(bits(y), bits(y0)) and torch.equal(bits(xn), bits(x0))
     q4a.check_device_error()
+
+
+def test_streams_of_different_kernels():
+    """Products for few and for many rows and a 4-bit product on the tensor cores, which all hold TMEM, on
+    three streams at the same time: what each gives alone."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(3)
+    few, many = device_operands(gen, 16, 4096, 4096), device_operands(gen, 2000, 8192, 2048)
+    rng = np.random.default_rng(3)
+    packed = torch.from_numpy(rng.integers(0, 256, (12288, 1024)).astype(np.uint8)).to(DEV)
+    sb = [torch.randn(12288, 32, device=DEV, generator=gen).to(torch.bfloat16) for _ in range(2)]
+    x = torch.randn(64, 2048, device=DEV, generator=gen).half()
+    alone = [q4a.gemm_fp8(*few), q4a.gemm_fp8(*many), q4a.gemv(packed, *sb, x)]
+    outs = [torch.empty_like(a) for a in alone]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in alone]
+    for _ in range(90):
+        q4a.gemm_fp8(*few, out=outs[0], stream=streams[0])
+        q4a.gemm_fp8(*many, out=outs[1], stream=streams[1])
+        q4a.gemv(packed, *sb, x, out=outs[2], stream=streams[2])
+    torch.cuda.synchronize()
+    q4a.check_device_error()
+    for a, b in zip(alone, outs):
+        assert torch.equal(bits(a), bits(b))
 
 
 @pytest.mark.parametrize("nb", [1, 16, 128, 500])
