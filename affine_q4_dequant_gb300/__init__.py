@@ -659,7 +659,7 @@ def gemv_kernel_choice(s, b, nb: int, out_dim: int, in_dim: int) -> str:
 
 
 def debug_withhold_stage(stage: int) -> None:
-    """Failure-path testing: the next GEMV-kernel launch from this thread never loads weight
+    """Failure-path testing: the next GEMV-kernel or 8-bit product launch from this thread never loads weight
     stage `stage` of each CTA, so its bounded wait gives up (check_device_error then raises
     ERR_TIMEOUT). -1 clears the request."""
     _check("q4a_debug_withhold_stage", _lib.q4a_debug_withhold_stage(int(stage)))

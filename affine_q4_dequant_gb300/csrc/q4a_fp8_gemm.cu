@@ -96,6 +96,7 @@ struct NarrowParams {
     int32_t nk;            // column blocks
     int32_t n_tiles;       // tiles of N activation rows
     int32_t cluster;
+    int32_t withhold_block;   // failure-path testing: block of a CTA never loaded, -1 none
     int32_t y_vec;         // rows of y allow 4-element stores
 };
 
@@ -216,9 +217,13 @@ __global__ void __launch_bounds__(kNwThreads, Narrow<N, T>::R) narrow_kernel(con
 
     if (warp == 0) {
         if (lane == 0) {
+            uint32_t used = 0, parity = 0;   // by stage: loaded at all, parity of its last load's phase
             for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
                 const int s = i % S;
                 if (i >= S) mbar_wait(smem_addr(empty + s), (uint32_t)(i / S - 1) & 1u, abort_flag);
+                if (i == p.withhold_block || *abort_flag) continue;   // after a give-up no new copies
+                parity ^= (used >> s & 1u) << s;
+                used |= 1u << s;
                 const uint32_t bar = smem_addr(full + s), at = smem_addr(smem + G::ring + s * G::stage);
                 mbar_arrive_expect_tx(bar, G::stage);
                 tma_load_2d(at, &p.tmap_w, kb * kFp8Block, (int)o0, bar);
@@ -227,8 +232,8 @@ __global__ void __launch_bounds__(kNwThreads, Narrow<N, T>::R) narrow_kernel(con
             }
             // after a give-up nobody has waited for the last copies: none may land after the CTA is gone
             if (*abort_flag)
-                for (int i = kb1 - kb0 < S ? 0 : kb1 - kb0 - S; i < kb1 - kb0; ++i)
-                    mbar_drain(smem_addr(full + i % S), (uint32_t)(i / S) & 1u);
+                for (int s = 0; s < S; ++s)
+                    if (used >> s & 1u) mbar_drain(smem_addr(full + s), parity >> s & 1u);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -476,6 +481,7 @@ q4a_status launch_narrow(const Fp8Gemm& g, int cluster, cudaStream_t stream) {
     p.nk = (int32_t)((g.in_dim + kFp8Block - 1) / kFp8Block);
     p.n_tiles = (int32_t)((g.nb + N - 1) / N);
     p.cluster = cluster;
+    p.withhold_block = take_withhold_stage();
     const int64_t size = fp8_type_bytes(g.y_type);
     p.y_vec = g.out_dim % 4 == 0 && reinterpret_cast<uintptr_t>(g.y) % (4 * size) == 0;
     const int64_t ctas = (g.out_dim + 127) / 128 * p.n_tiles * cluster;

@@ -58,6 +58,7 @@ struct WideParams {
     int32_t nk;            // column blocks
     int32_t m_tiles, n_tiles;
     int32_t k_split;       // first column block of the second pair (kernels with SPLIT; a multiple of 4)
+    int32_t withhold_block;   // failure-path testing: block of a CTA's first tile never loaded, -1 none
     int32_t xs_vec;        // rows of x_scale allow 16-byte copies
 };
 
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(kWdThreads, 1)
                                       : (wb0 + 1 < (p.g.out_dim + 127) / 128 ? wb0 + 1 : wb0);
             for (int kb = kb0; kb < kb1; ++kb) {
                 mbar_wait(empty + 8 * s, s_phase, abort_flag);
-                if (lane == 0) {
+                if (lane == 0 && (kb - kb0 != p.withhold_block || t != pair) && !*abort_flag) {   // after a give-up no new copies
                     if (leads) mbar_arrive_expect_tx(full + 8 * s, 2 * kWdStage);
                     const uint32_t lf = leader_addr(full + 8 * s, leader), at = base + s * kWdStage;
                     wd_tma_load(at, &p.tmap_x, kb * kFp8Block, (int)m0, lf);
@@ -445,12 +446,11 @@ __global__ void __launch_bounds__(kWdThreads, 1)
         if (TMA_Y && lane == 0) bulk_wait_all();   // no CTA exits while its y stores read shared memory
     }
 
-    // after a give-up no one has waited for the last copies and MMAs: they may not outlive the CTA
-    if (*abort_flag && warp == 1 && leads) {
-        int n = 0;
-        for (int t = pair; t < tiles; t += pairs) n += kb1 - kb0;
-        for (int i = n < kWdS ? 0 : n - kWdS; i < n; ++i) mbar_drain(full + 8 * (i % kWdS), (uint32_t)(i / kWdS) & 1u);
-        for (int i = n < 2 ? 0 : n - 2; i < n; ++i) mbar_drain(acc_full + 8 * (i & 1), (uint32_t)(i / 2) & 1u);
+    // After a give-up nobody has waited for the last copies and MMAs, and the pair's copies signal in the
+    // leader alone: this CTA, and with it the cluster, stays a millisecond, far longer than either takes.
+    if (*abort_flag && warp == 0) {
+        const uint64_t t0 = global_ns();
+        while (global_ns() - t0 < 1000000u) __nanosleep(1000);
     }
     __syncwarp();
     tc_fence_before();
@@ -511,6 +511,7 @@ q4a_status launch_gemm_fp8_wide(const Fp8Gemm& g, bool split, cudaStream_t strea
         if (r != CUDA_SUCCESS) return cuda_fail_drv(r);
     }
     p.k_split = (p.nk / 2 + 3) / 4 * 4;
+    p.withhold_block = take_withhold_stage();
     auto kernel = split ? wide_out<true>(g, tma_y) : wide_out<false>(g, tma_y);
     st = fp8_allow_smem(kernel, dev, kWdSmem);
     if (st != Q4A_OK) return st;

@@ -465,6 +465,9 @@ Q4A_API q4a_status q4a_dequant_fp8(uint8_t* w8, float* w_scale, const uint8_t* w
  * q4a_gemm_fp8 -- y = W.x on block-scaled 8-bit operands:
  *     y[r][o] = sum_k x_scale[r][k] * w_scale[o/128][k] * sum_{i in block k} x[r][i] * w[o][i]
  *   Products and sums of codes on the tensor cores, scales and the sum over blocks in fp32.
+ *   The kernel, its tiles and the split of the blocks follow from the sizes (and from whether rows of
+ *   y are multiples of 16 bytes), by estimated time. The same call gives the same bits; a row's last
+ *   bits may differ between batches of other sizes, whose blocks are summed in another grouping.
  *   y                 out  y_type [nb][out_dim], rounded once
  *   w, w_scale        in   e4m3 weights and their scales
  *   x, x_scale        in   e4m3 activations and their scales
@@ -521,12 +524,13 @@ Q4A_API int q4a_gemv_kernel_choice(const uint16_t* s, const uint16_t* b, int nb,
 
 /*
  * q4a_debug_withhold_stage -- a hook for testing the failure path: the next launch of the
- * GEMV kernel made from this host thread (any q4a_gemv* entry point whose work runs there;
- * not the tensor-core path) never loads weight stage `stage` of each CTA (counted from 0), so
- * its consumer warps give up their bounded wait on it after about a second, finish the launch
- * with garbage outputs, and q4a_check_device_error then reports Q4A_ERR_TIMEOUT. The kernel
- * issues no copy after the give-up and waits for the copies it already issued before it
- * exits. stage = -1 clears a pending request. Returns Q4A_ERR_SHAPE for stage < -1.
+ * GEMV kernel or of an 8-bit product made from this host thread (any q4a_gemv* entry point whose
+ * work runs on that kernel, not the tensor-core path; any q4a_gemm_fp8* one) never loads weight
+ * stage `stage` of each CTA (counted from 0; of its first tile in an 8-bit product), so its consumer
+ * warps give up their bounded wait on it after about a second, finish the launch with garbage
+ * outputs, and q4a_check_device_error then reports Q4A_ERR_TIMEOUT. The kernel waits for the copies
+ * it issued before it exits (the GEMV kernel issues none after the give-up). stage = -1 clears a
+ * pending request. Returns Q4A_ERR_SHAPE for stage < -1.
  */
 Q4A_API q4a_status q4a_debug_withhold_stage(int stage);
 

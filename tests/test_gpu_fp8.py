@@ -16,6 +16,8 @@ Bars, from the arithmetic:
   the product by half of one).
 """
 
+import time
+
 import numpy as np
 import pytest
 
@@ -579,6 +581,27 @@ def test_streams_of_different_kernels():
     q4a.check_device_error()
     for a, b in zip(alone, outs):
         assert torch.equal(bits(a), bits(b))
+
+
+@pytest.mark.parametrize("nb,out_dim,in_dim", [(8, 640, 2048), (16, 40000, 512), (2000, 8192, 1024), (300, 4096, 8192)])
+def test_withheld_stage_times_out_and_the_next_call_is_clean(nb, out_dim, in_dim):
+    """A block that is never loaded (split over a cluster, one CTA a tile, a pair of SMs and two pairs a
+    tile): the waits end, the status says so, and the same call is right afterwards."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(nb)
+    ops = device_operands(gen, nb, out_dim, in_dim)
+    clean = q4a.gemm_fp8(*ops)
+    q4a.check_device_error()
+    q4a.debug_withhold_stage(1)
+    t0 = time.perf_counter()
+    q4a.gemm_fp8(*ops)
+    with pytest.raises(q4a.Q4AError) as err:
+        q4a.check_device_error()
+    assert err.value.status_name == "ERR_TIMEOUT"
+    assert time.perf_counter() - t0 < 30.0
+    again = q4a.gemm_fp8(*ops)
+    q4a.check_device_error()
+    assert torch.equal(again, clean)
 
 
 @pytest.mark.parametrize("nb", [1, 16, 128, 500])
