@@ -82,7 +82,12 @@ struct Narrow {
     static constexpr int slot = bars + (2 * S + 3 * AB) * 8;
     static constexpr int abort = slot + 4;
     static constexpr int total = abort + 4;
-    static constexpr int smem = total + 1024;
+    // R == 2: just under half an SM, whatever the ring takes. Kernels of other streams and the next one
+    // of this stream start beside these CTAs before they have their TMEM, so what may share an SM must
+    // never ask for more than the 512 columns: two of these fit, a third does not, nor the other
+    // tensor-core kernels, which all take more than half.
+    static constexpr int smem = R == 2 ? 112 * 1024 : total + 1024;
+    static_assert(total + 1024 <= smem, "the ring's share");
     static_assert(S >= 2 && AB >= 2, "double buffering");
     static_assert(T * N * 512 <= S * stage, "the partial sums reuse the ring");
     static_assert(AB * T * N <= 512 / R, "TMEM of R CTAs");
