@@ -141,9 +141,10 @@ _ANY = None   # any dtype (prefetch hints)
 
 def _ptrs(*specs):
     """Device pointers for specs (tensor, name, dtypes, shape); a spec may be None (a NULL
-    pointer) or the address of a buffer that the binding has just allocated. A mis-shaped buffer would be read or written past its end by the kernels, so it is
-    refused here, before anything launches. This runs on every call: one pass over plain
-    comparisons and C-level tensor queries, and _refuse finds what to say where one fails."""
+    pointer) or the address of a buffer that the binding has just allocated. A mis-shaped buffer
+    would be read or written past its end by the kernels, so it is refused here, before anything
+    launches. This runs on every call: one pass over plain comparisons and C-level tensor queries,
+    and _refuse finds what to say where one fails."""
     out = []
     try:
         dev = _cuda_device()
@@ -508,7 +509,7 @@ def moe_combine(y: torch.Tensor, slot: torch.Tensor, w: torch.Tensor, y_shared: 
 
 def _type(t, name: str) -> int:
     """The q4a_type of a tensor (or dtype) that an 8-bit entry point takes in more than one type."""
-    dtype = t if t.__class__ is torch.dtype else t.dtype
+    dtype = t if t.__class__ is torch.dtype else getattr(t, "dtype", None)
     code = _TYPES.get(dtype)
     if code is None:
         raise TypeError(f"{name}: dtype {dtype} not in {tuple(_TYPES)}")

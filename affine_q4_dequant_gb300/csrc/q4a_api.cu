@@ -2,6 +2,7 @@
 // dispatch to the kernels. Every check runs on the host before anything is launched.
 #include <string.h>
 
+#include <initializer_list>
 #include <vector>
 
 #include "q4a_fp8.h"
@@ -581,6 +582,29 @@ bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
     return x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
 }
 
+struct Span {
+    const void* p;   // NULL for a buffer that is not there
+    int64_t n;
+};
+
+// Whether no output shares a byte with another output or with an input.
+bool apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+    for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+        if (!o->p) continue;
+        for (const Span* q = o + 1; q != outs.end(); ++q)
+            if (q->p && overlap(o->p, o->n, q->p, q->n)) return false;
+        for (const Span& i : ins)
+            if (i.p && overlap(o->p, o->n, i.p, i.n)) return false;
+    }
+    return true;
+}
+
+int64_t blocks(int64_t dim) { return (dim + kFp8Block - 1) / kFp8Block; }
+Span codes(const uint8_t* q, int64_t rows, int64_t dim) { return {q, rows * dim}; }
+Span row_scales(const float* s, int64_t rows, int64_t dim) { return {s, rows * blocks(dim) * 4}; }
+Span block_scales(const float* s, int64_t rows, int64_t dim) { return {s, blocks(rows) * blocks(dim) * 4}; }
+Span rows_of(const void* p, q4a_type t, int64_t rows, int64_t dim) { return {p, rows * dim * fp8_type_bytes(t)}; }
+
 // Rows of 8-bit activations: sizes and the two output (or input) buffers.
 q4a_status check_fp8_rows(const uint8_t* q, const float* scale, int64_t nb, int64_t dim) {
     if (!q || !scale) return Q4A_ERR_NULL;
@@ -661,6 +685,7 @@ q4a_status q4a_quantize_fp8(uint8_t* q, float* scale, const void* x, q4a_type x_
     if (st != Q4A_OK) return st;
     if (!type_ok(x_type)) return Q4A_ERR_SHAPE;
     if (!aligned(x, 16)) return Q4A_ERR_ALIGN;
+    if (!apart({codes(q, nb, dim), row_scales(scale, nb, dim)}, {rows_of(x, x_type, nb, dim)})) return Q4A_ERR_SHAPE;
     Fp8Norm n = {};
     n.q = q;
     n.scale = scale;
@@ -676,7 +701,13 @@ q4a_status q4a_add_rmsnorm_fp8(uint8_t* q, float* scale, void* x_new, const void
                                float shift, int64_t nb, int64_t dim, q4a_stream_t stream) {
     const Fp8Norm n = {q, scale, x_new, x, x_type, residual, res_type, norm_w, eps, shift, nb, dim};
     const q4a_status st = check_add_rmsnorm(n);
-    return st != Q4A_OK ? st : launched([&] { return launch_fp8_rows(n, (cudaStream_t)stream); });
+    if (st != Q4A_OK) return st;
+    const Span qs = codes(q, nb, dim), ss = row_scales(scale, nb, dim), xn = rows_of(x_new, res_type, nb, dim),
+               w = {norm_w, dim * 2};
+    if (!apart({qs, ss, xn}, {w}) ||
+        !apart({qs, ss}, {rows_of(x, x_type, nb, dim), rows_of(residual, res_type, nb, dim)}))
+        return Q4A_ERR_SHAPE;   // (x_new on x or the residual: looked at above)
+    return launched([&] { return launch_fp8_rows(n, (cudaStream_t)stream); });
 }
 
 q4a_status q4a_dequant_fp8(uint8_t* w8, float* w_scale, const uint8_t* w, const uint16_t* s, const uint16_t* b,
@@ -686,6 +717,10 @@ q4a_status q4a_dequant_fp8(uint8_t* w8, float* w_scale, const uint8_t* w, const 
     if (st != Q4A_OK) return st;
     if (!aligned(w8, 16) || !aligned(w_scale, 4) || !aligned(w, 16) || !aligned(s, 2) || !aligned(b, 2))
         return Q4A_ERR_ALIGN;
+    const int64_t groups = rows * (in_dim / 64) * 2;
+    if (!apart({codes(w8, rows, in_dim), block_scales(w_scale, rows, in_dim)},
+               {{w, rows * (in_dim / 2)}, {s, groups}, {b, groups}}))
+        return Q4A_ERR_SHAPE;
     return launched([&] { return launch_dequant_fp8(w8, w_scale, w, s, b, rows, in_dim, (cudaStream_t)stream); });
 }
 
@@ -693,7 +728,11 @@ q4a_status q4a_gemm_fp8(void* y, q4a_type y_type, const uint8_t* w, const float*
                         const float* x_scale, int64_t nb, int64_t out_dim, int64_t in_dim, q4a_stream_t stream) {
     const Fp8Gemm g = {y, y_type, nullptr, nullptr, w, w_scale, x, x_scale, nb, out_dim, in_dim};
     const q4a_status st = check_gemm_fp8(g);
-    return st != Q4A_OK ? st : launched([&] { return launch_gemm_fp8(g, (cudaStream_t)stream); });
+    if (st != Q4A_OK) return st;
+    if (!apart({rows_of(y, y_type, nb, out_dim)}, {codes(w, out_dim, in_dim), block_scales(w_scale, out_dim, in_dim),
+                                                   codes(x, nb, in_dim), row_scales(x_scale, nb, in_dim)}))
+        return Q4A_ERR_SHAPE;
+    return launched([&] { return launch_gemm_fp8(g, (cudaStream_t)stream); });
 }
 
 q4a_status q4a_gemm_fp8_gate_up_silu(uint8_t* q, float* scale, const uint8_t* w, const float* w_scale,
@@ -701,7 +740,12 @@ q4a_status q4a_gemm_fp8_gate_up_silu(uint8_t* q, float* scale, const uint8_t* w,
                                      int64_t in_dim, q4a_stream_t stream) {
     const Fp8Gemm g = {nullptr, Q4A_F32, q, scale, w, w_scale, x, x_scale, nb, inter, in_dim};
     const q4a_status st = check_gate_up_fp8(g);
-    return st != Q4A_OK ? st : launched([&] { return launch_gemm_fp8(g, (cudaStream_t)stream); });
+    if (st != Q4A_OK) return st;
+    if (!apart({codes(q, nb, inter), row_scales(scale, nb, inter)},
+               {codes(w, 2 * inter, in_dim), block_scales(w_scale, 2 * inter, in_dim), codes(x, nb, in_dim),
+                row_scales(x_scale, nb, in_dim)}))
+        return Q4A_ERR_SHAPE;
+    return launched([&] { return launch_gemm_fp8(g, (cudaStream_t)stream); });
 }
 
 q4a_status q4a_mlp_fp8(void* y, q4a_type y_type, void* x_new, uint8_t* n, float* n_scale, uint8_t* h,
@@ -716,6 +760,13 @@ q4a_status q4a_mlp_fp8(void* y, q4a_type y_type, void* x_new, uint8_t* n, float*
     if (st == Q4A_OK) st = check_gate_up_fp8(gu);
     if (st == Q4A_OK) st = check_gemm_fp8(dn);
     if (st != Q4A_OK) return st;
+    const Span ys = rows_of(y, y_type, nb, hidden), xn = rows_of(x_new, res_type, nb, hidden),
+               ns = codes(n, nb, hidden), nss = row_scales(n_scale, nb, hidden), hs = codes(h, nb, inter),
+               hss = row_scales(h_scale, nb, inter), w = {norm_w, hidden * 2};
+    if (!apart({ys, xn, ns, nss, hs, hss}, {w, codes(w_gu, 2 * inter, hidden), block_scales(ws_gu, 2 * inter, hidden),
+                                            codes(w_dn, hidden, inter), block_scales(ws_dn, hidden, inter)}) ||
+        !apart({ys, ns, nss, hs, hss}, {rows_of(x, x_type, nb, hidden), rows_of(residual, res_type, nb, hidden)}))
+        return Q4A_ERR_SHAPE;
     return launched([&] {
         q4a_status s = launch_fp8_rows(norm, (cudaStream_t)stream);
         if (s == Q4A_OK) s = launch_gemm_fp8(gu, (cudaStream_t)stream);

@@ -411,13 +411,13 @@ Q4A_API q4a_status q4a_moe_combine(float* out, const float* y, const int32_t* sl
  *                w_scale [ceil(out_dim/128)][ceil(in_dim/128)]
  *   The value is code * scale. Where this library writes scales, a block of values v gets
  *       scale = max(max|v|, 2^-100) / 448,   code = e4m3(v * (1 / scale)), round to nearest even,
- *   in fp32 (the scale and 1 / scale to a unit in the last place); a block of zeros has scale 2^-100 / 448 and zero codes. The scales that a product
- *   reads are any fp32 values. The last block of a row or column may be short. A NaN becomes a
- *   NaN code and leaves its block's scale to the other values; an infinity makes its block's
- *   scale infinite: either comes out of a product as NaN.
+ *   in fp32 (the scale and 1 / scale to a unit in the last place); a block of zeros has scale
+ *   2^-100 / 448 and zero codes. The scales that a product reads are any fp32 values. The last block
+ *   of a row or column may be short. A NaN becomes a NaN code and leaves its block's scale to the
+ *   other values; an infinity makes its block's scale infinite: either comes out of a product as NaN.
  *   Rows are multiples of 16 bytes: dim, in_dim and inter are multiples of 16 (the products fetch
- *   them with tensor copies). An output overlaps neither an input nor another output, but for x_new
- *   where it says so.
+ *   them with tensor copies). An output overlaps neither an input nor another output (else
+ *   Q4A_ERR_SHAPE), but for x_new where it says so.
  *
  * q4a_quantize_fp8 -- activations in 8 bits.
  *   q      out  e4m3 [nb][dim]
@@ -435,7 +435,8 @@ Q4A_API q4a_status q4a_quantize_fp8(uint8_t* q, float* scale, const void* x, q4a
  * fn_group_norm_b, one normalisation group).
  *     x'[r][i] = residual type( x[r][i] + residual[r][i] )      (x itself without a residual)
  *     n[r][i]  = x'[r][i] * (mean_i x'[r][i]^2 + eps)^(-1/2) * (norm_w[i] + shift),  in 8 bits
- *   The sum is rounded to fp32, then to the residual's type; the norm reads the stored value.
+ *   The sum is rounded to fp32, then to the residual's type; the norm reads the stored value. The
+ *   squares are summed in fp32: a row whose sum leaves its range becomes zeros.
  *   q, scale   out  as q4a_quantize_fp8
  *   x_new      out  res_type [nb][dim], x'; may be NULL, the same buffer as residual (in place)
  *                   or, with x_type == res_type, as x. Any other overlap is Q4A_ERR_SHAPE, and so
@@ -484,7 +485,8 @@ Q4A_API q4a_status q4a_gemm_fp8(void* y, q4a_type y_type, const uint8_t* w, cons
  * epilogue and an 8-bit output, the down product's input ("BATCH_MSL", experts.metal
  * fn_moe_gate_up_b followed by fn_moe_act_b):
  *     h[r][o] = silu(g) * u,  g = (W_gate.x)[r][o],  u = (W_up.x)[r][o],  silu(v) = v / (1 + e^-v)
- *   g, u and h in fp32; no wider h exists.
+ *   g, u and h in fp32; no wider h exists. Below g = -87, where 1 / (1 + e^-g) leaves fp32's normal
+ *   range, silu(g) may be 0.
  *   q        out  e4m3 [nb][inter]
  *   scale    out  fp32 [nb][inter/128]
  *   w        in   e4m3 [2*inter][in_dim]: gate rows, then up rows; w_scale [2*inter/128][ceil(in_dim/128)]

@@ -149,3 +149,57 @@ def test_binding_refusals(q4a):
     _bad(lambda: mod.mlp_fp8(x, nw, g, gs, d, ds, h=(torch.zeros(2, 64, dtype=f8), None)), "h: shape")
     _bad(lambda: mod.mlp_fp8(x, nw, g, gs, d, ds, x_new=x), "needs a residual")
     _bad(lambda: mod.mlp_fp8(x, nw, g, gs, d, ds), "CUDA", TypeError)
+
+
+def test_overlaps_are_refused(lib):
+    """An output on an input or on another output, by their first or last bytes."""
+    step = 1 << 24
+    at = lambda i, off=0: (i + 1) * step + off   # noqa: E731
+
+    def quant(q=at(0), s=at(1), x=at(2)):
+        return lib.q4a_quantize_fp8(q, s, x, F32, 2, 256, None)
+
+    assert quant(q=at(2)) == quant(q=at(2, 2032)) == quant(s=at(2, 1024)) == quant(s=at(0, 508)) == SHAPE
+
+    def norm(q=at(0), s=at(1), xn=at(2), x=at(3), r=at(4), w=at(5)):
+        return lib.q4a_add_rmsnorm_fp8(q, s, xn, x, F32, r, F32, w, 1e-6, 0.0, 2, 256, None)
+
+    assert norm(q=at(2)) == norm(q=at(3)) == norm(q=at(4, 2032)) == norm(s=at(5)) == norm(xn=at(5, -2032)) == SHAPE
+
+    def dequant(o=at(0), c=at(1), w=at(2), s=at(3), b=at(4)):
+        return lib.q4a_dequant_fp8(o, c, w, s, b, 4, 128, None)
+
+    assert dequant(o=at(2)) == dequant(o=at(2, -496)) == dequant(c=at(3)) == dequant(c=at(4, 12)) == dequant(c=at(0)) == SHAPE
+
+    def gemm(y=at(0), w=at(1), ws=at(2), x=at(3), xs=at(4)):
+        return lib.q4a_gemm_fp8(y, F32, w, ws, x, xs, 2, 8, 128, None)
+
+    assert gemm(y=at(1, 1020)) == gemm(y=at(2)) == gemm(y=at(3)) == gemm(y=at(4, -60)) == SHAPE
+
+    def gate(q=at(0), s=at(1), w=at(2), ws=at(3), x=at(4), xs=at(5)):
+        return lib.q4a_gemm_fp8_gate_up_silu(q, s, w, ws, x, xs, 2, 128, 128, None)
+
+    assert gate(q=at(4)) == gate(q=at(2, 32752)) == gate(s=at(0)) == gate(s=at(5, 4)) == gate(s=at(3)) == SHAPE
+
+    def mlp(y=at(0), xn=at(1), n=at(2), ns=at(3), h=at(4), hs=at(5), x=at(6), r=at(7), nw=at(8), wg=at(9), sg=at(10),
+            wd=at(11), sd=at(12)):
+        return lib.q4a_mlp_fp8(y, F32, xn, n, ns, h, hs, x, F32, r, F32, nw, 1e-6, 0.0, wg, sg, wd, sd, 2, 128, 128, None)
+
+    for a, b in (("y", "xn"), ("y", "n"), ("y", "x"), ("y", "r"), ("n", "h"), ("ns", "hs"), ("h", "x"), ("hs", "nw"),
+                 ("xn", "wg"), ("n", "sg"), ("h", "wd"), ("y", "sd")):
+        i = ("y", "xn", "n", "ns", "h", "hs", "x", "r", "nw", "wg", "sg", "wd", "sd").index(b)
+        assert mlp(**{a: at(i)}) == SHAPE, (a, b)
+
+
+def test_binding_refuses_what_is_no_tensor(q4a):
+    mod, torch = q4a
+    x, nw = torch.zeros(2, 128), torch.zeros(128, dtype=torch.bfloat16)
+    w, ws = torch.zeros(64, 128, dtype=torch.float8_e4m3fn), torch.zeros(1, 1)
+    xq, xs = torch.zeros(2, 128, dtype=torch.float8_e4m3fn), torch.zeros(2, 1)
+    _bad(lambda: mod.quantize_fp8([1.0]), "x must be a tensor", TypeError)
+    _bad(lambda: mod.quantize_fp8(x, q=[0]), "q must be a", TypeError)
+    _bad(lambda: mod.add_rmsnorm_fp8(x, nw, residual=[0.0]), "residual", TypeError)
+    _bad(lambda: mod.add_rmsnorm_fp8(x, None), "norm_w must be a", TypeError)
+    _bad(lambda: mod.gemm_fp8(w, ws, xq, xs, out=[0.0]), "y", TypeError)
+    _bad(lambda: mod.gemm_fp8(w, ws, xq, xs, out_dtype="bf16"), "y", TypeError)
+    _bad(lambda: mod.gemm_fp8(w, None, xq, xs), "w_scale must be a", TypeError)
